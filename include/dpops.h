@@ -1,0 +1,167 @@
+/*
+ * dpops.h -- C ABI of the training-pass operators of libdpstep.so (sm_103a).
+ *
+ * dpstep.h reduces gradients that lie in flat bf16 rank buffers and updates
+ * the parameters.  The operators here are parts of the forward and backward
+ * passes that fill those buffers: the embedding lookup and its gradient, the
+ * norms around a block fused with its gate and residual scale, activation
+ * checkpoints in 8 bits with the gated activation and the weight gradient that
+ * use them.  Parameters are read from, and parameter gradients written to (or
+ * added to), any element offset of a flat buffer.
+ *
+ * Conventions, beside those of dpstep.h (asynchronous on the caller's stream,
+ * no allocation, no host synchronisation, a call that returns an error has
+ * launched nothing):
+ *  - A device pointer needs the alignment of its own element type only, unless
+ *    its description says more; rows that are 16-byte aligned take wider loads.
+ *  - Sums, statistics and norms are held in fp32; each output is rounded once.
+ *  - Orders of summation are fixed: results are bit-identical run to run.
+ *  - Outputs must not overlap inputs or each other, except where a description
+ *    says so.
+ *  - A workspace (256-byte aligned) may be used again by the next call on the
+ *    same stream; its contents mean nothing between calls.
+ *  - "Write or add": with accumulate = 0 an output is overwritten; with
+ *    accumulate = 1 the result is added to what it holds, the sum taken in
+ *    fp32 and rounded once.
+ */
+#ifndef DPOPS_H
+#define DPOPS_H
+
+#include "dpstep.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of the operators' tensors. */
+enum { DP_BF16 = 0, DP_F32 = 1 };
+
+/* ---- embedding lookup ------------------------------------------------------ */
+
+/* out[t][:] = scale * table[ids[t]][:], t < tokens; a row of zeros where
+ * ids[t] is outside [0, vocab).
+ * table: [vocab][dim]; out: [tokens][dim]; both of `dtype`; ids: int32
+ * (id_bits 32) or int64 (id_bits 64).  vocab, tokens < 2^31. */
+dp_status_t dp_embedding(void* out, const void* table, const void* ids, int64_t tokens, int64_t vocab, int64_t dim,
+                         float scale, int32_t dtype, int32_t id_bits, dp_stream_t stream);
+
+/* Bytes of workspace of dp_embedding_grad; 0 on a bad size. */
+size_t dp_embedding_workspace_size(int64_t tokens, int64_t vocab, int64_t dim);
+
+/* The gradient of dp_embedding with respect to its table (write or add):
+ *   dtable[v][:] (+)= scale * sum over t with ids[t] = v of dout[t][:]
+ * pad_id (any value, -1 for none): tokens with this id give no gradient, and
+ * neither do ids outside [0, vocab).  Written: rows that no token names are
+ * set to zero.  Added: such rows are neither read nor written.  A row's tokens
+ * are added in a fixed order (the tokens sorted by id, equal ids in order). */
+dp_status_t dp_embedding_grad(void* dtable, const void* dout, const void* ids, int64_t tokens, int64_t vocab,
+                              int64_t dim, float scale, int64_t pad_id, int32_t accumulate, int32_t dtype,
+                              int32_t id_bits, void* ws, dp_stream_t stream);
+
+/* ---- the norms around a block ---------------------------------------------- */
+
+enum { DP_NORM_RMS = 0, DP_NORM_LAYER = 1 };                              /* kind */
+enum { DP_GATE_NONE = 0, DP_GATE_CHANNEL = 1, DP_GATE_TOKEN = 2 };        /* gate_mode */
+enum { DP_NORM_POST = 1, DP_NORM_PRE = 2 };                               /* norms */
+enum { DP_MAX_NORM_DIM = 16384 };
+
+/* A block boundary of a residual network: the block's output y goes through a
+ * norm of its own, a gate and a scale into the residual stream, and the stream
+ * through the norm before the next block:
+ *   r = res_scale * x + branch_scale * gate * N_post(y)
+ *   z = N_pre(r)
+ *   N(v) = (v - mean) * rstd * w + b,  rstd = 1 / sqrt(var + eps)
+ * RMS: mean = 0 and var = the mean of v^2.  Layer: the row's mean and (biased)
+ * variance.  gate: [dim] (channel), [rows] (token), or none.  Without
+ * DP_NORM_POST, N_post(y) = y.  Without DP_NORM_PRE there is no z.  y = NULL:
+ * there is no block yet, r is x itself (res_scale must be 1, r NULL), z =
+ * N_pre(x). */
+typedef struct {
+  int64_t rows;
+  int32_t dim;           /* 1..DP_MAX_NORM_DIM */
+  int32_t kind, norms, gate_mode;
+  int32_t stream_dtype;  /* x, r, dr, dx */
+  int32_t block_dtype;   /* y, z, dy, dz; DP_F32 only with a DP_F32 stream */
+  int32_t param_dtype;   /* weights, biases, gate and their gradients */
+  int32_t accumulate;    /* of the parameter gradients */
+  float eps;             /* > 0 (the gradient does not use it) */
+  float res_scale, branch_scale;
+} dp_block_norm_t;
+
+/* Forward.  w_post, b_post, w_pre, b_pre: [dim], NULL for ones (zeros).
+ * post_stats, pre_stats: [rows][2] fp32, each row's (mean, rstd) for the
+ * gradient; written for the norms that are there; may be NULL.  z is taken from
+ * the r that is not rounded yet.  r may be x. */
+dp_status_t dp_block_norm(const dp_block_norm_t* p, void* r, void* z, const void* x, const void* y,
+                          const void* w_post, const void* b_post, const void* gate, const void* w_pre,
+                          const void* b_pre, float* post_stats, float* pre_stats, dp_stream_t stream);
+
+/* Bytes of workspace of dp_block_norm_grad; 0 on a bad size. */
+size_t dp_block_norm_workspace_size(int64_t rows, int64_t dim);
+
+/* Gradient: dr (of r, from the rest of the stream; NULL for zeros) and dz (of
+ * z) in, dx and dy out; with D = dr + N_pre'(dz):
+ *   dx = res_scale * D,  dy = N_post'(branch_scale * gate * D)
+ * and the parameters' gradients, each written or added unless NULL.  dgate has
+ * the gate's shape.  r and y: the forward's, with its statistics (r as it was
+ * stored; without y, r is x).  dx may be dr, dy may be dz or y. */
+dp_status_t dp_block_norm_grad(const dp_block_norm_t* p, void* dx, void* dy, const void* dr, const void* dz,
+                               const void* r, const void* y, const void* w_post, const void* b_post, const void* gate,
+                               const void* w_pre, const float* post_stats, const float* pre_stats, void* dw_post,
+                               void* db_post, void* dgate, void* dw_pre, void* db_pre, void* ws, dp_stream_t stream);
+
+/* ---- activation checkpoints in 8 bits --------------------------------------- */
+
+/* A row of `dim` values is kept as dp_ckpt8_pitch(dim) int8 codes and one step
+ * byte for each group of 32 of them (the last group filled up with zero codes).
+ * A group's step is a power of two, 2^(E - 127) for the byte E in 1..254: the
+ * least for which all codes round(x / step) (ties to even) are within +-127;
+ * E = 1 for a group of zeros.  A group that holds an infinity or a NaN has
+ * E = 255 and stands for NaNs, so that an overflow reaches the gradients and
+ * skips the step.  A code times its step has at most 7 bits: the value is exact
+ * in bf16.  codes: [rows][pitch] int8, 16-byte aligned; scales: [rows][pitch /
+ * 32] bytes. */
+enum { DP_CKPT8_GROUP = 32 };
+int64_t dp_ckpt8_pitch(int64_t dim); /* dim rounded up to a multiple of 32; -1 if dim < 1 */
+
+/* x: [rows][dim], row stride ldx elements, `dtype`. */
+dp_status_t dp_ckpt8_encode(int8_t* codes, uint8_t* scales, const void* x, int64_t rows, int64_t dim, int64_t ldx,
+                            int32_t dtype, dp_stream_t stream);
+dp_status_t dp_ckpt8_decode(void* x, const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t dim, int64_t ldx,
+                            int32_t dtype, dp_stream_t stream);
+
+/* f: SiLU g / (1 + e^-g), or GELU in its tanh form. */
+enum { DP_ACT_SILU = 0, DP_ACT_GELU = 1 };
+
+/* h = f(g) * u (u = NULL: h = f(g)), bf16, computed from g and u as given; and
+ * the checkpoints of g and u that the gradient reads (u8 = NULL with u = NULL).
+ * g and u: [rows][dim] with row stride ld (both halves of one product: ld =
+ * 2 dim); h: row stride ldh. */
+dp_status_t dp_act_ckpt8(uint16_t* h, const uint16_t* g, const uint16_t* u, int8_t* g8, uint8_t* g8_scales, int8_t* u8,
+                         uint8_t* u8_scales, int64_t rows, int64_t dim, int64_t ld, int64_t ldh, int32_t act,
+                         dp_stream_t stream);
+
+/* With g and u as their checkpoints stand for them:
+ *   dg = dh * u * f'(g),  du = dh * f(g),  h = f(g) * u
+ * h (the activation again, for the weight gradient of the product that follows;
+ * may be NULL) and dh: row stride ldh; dg and du: row stride ld.  h may be dh. */
+dp_status_t dp_act_ckpt8_grad(uint16_t* dg, uint16_t* du, uint16_t* h, const uint16_t* dh, const int8_t* g8,
+                              const uint8_t* g8_scales, const int8_t* u8, const uint8_t* u8_scales, int64_t rows,
+                              int64_t dim, int64_t ld, int64_t ldh, int32_t act, dp_stream_t stream);
+
+/* Bytes of workspace of dp_wgrad8; 0 on a bad size (and where none is needed). */
+size_t dp_wgrad8_workspace_size(int64_t rows, int64_t n, int64_t k);
+
+/* Weight gradient of y = x W^T from the 8-bit checkpoint of x (write or add):
+ *   dw[i][j] (+)= alpha * sum over the rows m of dy[m][i] * x[m][j]
+ * dy: bf16 [rows][n], row stride lddy; codes, scales: the checkpoint of x
+ * [rows][k]; dw: [n][k], contiguous, `dtype`.  dy and the decoded x (both exact
+ * in bf16) are multiplied on the tensor cores and summed in fp32. */
+dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t n,
+                      int64_t k, int64_t lddy, float alpha, int32_t accumulate, int32_t dtype, void* ws,
+                      dp_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* DPOPS_H */

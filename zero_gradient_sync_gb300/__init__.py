@@ -2,7 +2,10 @@
 loss-scale unscaling and a global non-finite skip, ZeRO-partitioned mixed-precision Adam, and the bf16
 parameter all-gather -- all n replicas' buffers in one GPU's memory.
 
-The computation lives in libdpstep.so (CUDA, sm_103a; C ABI in include/dpstep.h).  This package is its
+Beside the step, the training-pass operators that fill its gradient buffers: embedding lookup and gradient, the norms around
+a block, 8-bit activation checkpoints with the gated activation and the weight gradient that use them.
+
+The computation lives in libdpstep.so (CUDA, sm_103a; C ABI in include/dpstep.h and include/dpops.h).  This package is its
 binding; importing it without the built library raises ImportError.
 """
 from ._lib import (  # noqa: F401
@@ -14,3 +17,8 @@ from ._lib import (  # noqa: F401
     dp_state_init, dp_step, dp_step_from_host, dp_step_reduce, dp_step_scaled, dp_step_single_pass,
     dp_step_single_pass_from_host, dp_step_static, dp_step_update,
     dp_traffic_model, new_state, read_state, scaler)
+from .ops import (  # noqa: F401
+    DP_ACT_GELU, DP_ACT_SILU, DP_BF16, DP_CKPT8_GROUP, DP_F32, DP_GATE_CHANNEL, DP_GATE_NONE, DP_GATE_TOKEN, DP_MAX_NORM_DIM,
+    DP_NORM_LAYER, DP_NORM_POST, DP_NORM_PRE, DP_NORM_RMS, dp_act_ckpt8, dp_act_ckpt8_grad, dp_block_norm,
+    dp_block_norm_grad, dp_block_norm_t, dp_block_norm_workspace_size, dp_ckpt8_decode, dp_ckpt8_encode, dp_ckpt8_pitch,
+    dp_embedding, dp_embedding_grad, dp_embedding_workspace_size, dp_wgrad8, dp_wgrad8_workspace_size, new_ckpt8)

@@ -11,8 +11,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdpstep.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["dp_api.cu", "dp_kernels.cu", "dp_static.cu", "dp_checkpoint.cu", "dp_tree.cu", "dp_tree_sp.cu",
-           "dp_micro.cu"]
-HEADERS = ["dp_device.cuh", "dp_internal.h", "dp_launch.h", "dp_single.cuh"]
+           "dp_micro.cu", "op_embedding.cu", "op_norm.cu", "op_ckpt8.cu", "op_wgrad8.cu"]
+HEADERS = ["dp_device.cuh", "dp_internal.h", "dp_launch.h", "dp_single.cuh", "op_common.cuh"]
+PUBLIC = ["dpstep.h", "dpops.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -23,7 +24,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "dpstep.h"), __file__]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, f) for f in PUBLIC] + [__file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -236,6 +236,8 @@ dp_status_t check_full_arrays(const Plan& P, const void* const* arr, int count, 
 
 dp_status_t dp::report_error(dp_status_t s, const char* msg) { return fail(s, "%s", msg); }
 
+void dp::add_launches(uint64_t n) { g_launches.fetch_add(n); }
+
 extern "C" {
 
 int32_t dp_abi_version(void) { return 2; }

@@ -91,6 +91,8 @@ struct NvtxRange {
 
 // Records msg as this thread's dp_last_error() and returns s.
 dp_status_t report_error(dp_status_t s, const char* msg);
+// Adds n to dp_kernel_launches().
+void add_launches(uint64_t n);
 
 // Each launcher returns the launch's cudaError_t and adds to *launches.
 cudaError_t launch_reduce(const Plan& P, const uint16_t* const* g, int a, float* const* gbar, const StepScalars& s,

@@ -1,0 +1,131 @@
+// What the training-pass operators share: element access in groups of eight, argument checks, launch counting.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdarg.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include "dp_device.cuh"
+#include "dp_internal.h"
+#include "dp_launch.h"
+#include "dpops.h"
+
+namespace dp {
+
+typedef uint16_t bf16_t;  // bit pattern
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<bf16_t> {
+  static __device__ __forceinline__ float get(bf16_t v) { return bf16_to_f32(v); }
+  static __device__ __forceinline__ bf16_t put(float v) { return bf16_rn(v); }
+};
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+
+// Eight elements as they lie in memory: one 16-byte word of bf16, two of fp32.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16_t> {
+  uint4 a;
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+    v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
+    v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+  }
+  __device__ __forceinline__ void pack(const float (&v)[8]) {
+    a.x = bf16x2_rn(v[0], v[1]); a.y = bf16x2_rn(v[2], v[3]);
+    a.z = bf16x2_rn(v[4], v[5]); a.w = bf16x2_rn(v[6], v[7]);
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ __forceinline__ void pack(const float (&v)[8]) {
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+
+// 16-byte aligned access to eight elements, once-read and once-written data past L1.
+__device__ __forceinline__ Raw8<bf16_t> load_raw8(const bf16_t* p) {
+  Raw8<bf16_t> r;
+  r.a = __ldcs(reinterpret_cast<const uint4*>(p));
+  return r;
+}
+__device__ __forceinline__ Raw8<float> load_raw8(const float* p) {
+  Raw8<float> r;
+  r.a = __ldcs(reinterpret_cast<const float4*>(p));
+  r.b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  return r;
+}
+__device__ __forceinline__ void store_raw8(bf16_t* p, const Raw8<bf16_t>& r) {
+  *reinterpret_cast<uint4*>(p) = r.a;
+}
+__device__ __forceinline__ void store_raw8(float* p, const Raw8<float>& r) {
+  reinterpret_cast<float4*>(p)[0] = r.a;
+  reinterpret_cast<float4*>(p)[1] = r.b;
+}
+
+// A parameter of either type, at any element offset; NULL stands for `none`.
+__device__ __forceinline__ float param_at(const void* p, int64_t i, int dtype, float none) {
+  if (!p) return none;
+  return dtype == DP_BF16 ? bf16_to_f32(__ldg(static_cast<const uint16_t*>(p) + i))
+                          : __ldg(static_cast<const float*>(p) + i);
+}
+// Writes v to (or adds it to) element i of a gradient of either type.
+__device__ __forceinline__ void grad_put(void* p, int64_t i, int dtype, int accumulate, float v) {
+  if (dtype == DP_BF16) {
+    uint16_t* q = static_cast<uint16_t*>(p) + i;
+    *q = bf16_rn(accumulate ? __fadd_rn(bf16_to_f32(*q), v) : v);
+  } else {
+    float* q = static_cast<float*>(p) + i;
+    *q = accumulate ? __fadd_rn(*q, v) : v;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+inline dp_status_t op_fail(dp_status_t s, const char* fmt, ...) {
+  char msg[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof(msg), fmt, ap);
+  va_end(ap);
+  return report_error(s, msg);
+}
+inline dp_status_t op_launched(const char* what, int n) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return op_fail(DP_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  add_launches((uint64_t)n);
+  return DP_OK;
+}
+inline int elem_size(int dtype) { return dtype == DP_F32 ? 4 : 2; }
+inline bool is_aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+inline dp_status_t check_dtype(int dtype, const char* name) {
+  if (dtype != DP_BF16 && dtype != DP_F32) return op_fail(DP_ERR_INVALID_ARG, "%s: element type %d unknown", name, dtype);
+  return DP_OK;
+}
+// A device pointer to elements of `size` bytes; needed: NULL is refused.
+inline dp_status_t check_dev(const void* p, size_t size, bool needed, const char* name) {
+  if (!p) return needed ? op_fail(DP_ERR_INVALID_ARG, "%s is NULL", name) : DP_OK;
+  if (!is_aligned(p, size)) return op_fail(DP_ERR_ALIGNMENT, "%s is not %d-byte aligned", name, (int)size);
+  return DP_OK;
+}
+
+}  // namespace dp
+
+#define DP_TRY(expr)                        \
+  do {                                      \
+    const dp_status_t try_status_ = (expr); \
+    if (try_status_ != DP_OK) return try_status_; \
+  } while (0)

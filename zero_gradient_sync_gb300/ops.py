@@ -1,0 +1,301 @@
+"""ctypes binding of the training-pass operators of libdpstep.so (include/dpops.h) under the same names.
+
+Argument marshalling only, as in _lib: the caller owns every buffer, calls are queued on the current stream (or
+`stream`), and the library's own checks raise DPError.  What the library cannot see -- devices, types, shapes, strides --
+is checked here and raises ValueError.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from ._lib import LIB, DPError, _check, _stream, c_f32, c_i32, c_i64, c_vp, DP_ERR_INVALID_ARG
+
+DP_BF16, DP_F32 = 0, 1
+DP_NORM_RMS, DP_NORM_LAYER = 0, 1
+DP_GATE_NONE, DP_GATE_CHANNEL, DP_GATE_TOKEN = 0, 1, 2
+DP_NORM_POST, DP_NORM_PRE = 1, 2
+DP_MAX_NORM_DIM = 16384
+DP_CKPT8_GROUP = 32
+DP_ACT_SILU, DP_ACT_GELU = 0, 1
+
+
+class dp_block_norm_t(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("dim", c_i32), ("kind", c_i32), ("norms", c_i32), ("gate_mode", c_i32),
+                ("stream_dtype", c_i32), ("block_dtype", c_i32), ("param_dtype", c_i32), ("accumulate", c_i32),
+                ("eps", c_f32), ("res_scale", c_f32), ("branch_scale", c_f32)]
+
+
+def _declare() -> None:
+    size_t, P = ctypes.c_size_t, ctypes.POINTER(dp_block_norm_t)
+    sig = {
+        "dp_embedding": (c_i32, [c_vp] * 3 + [c_i64] * 3 + [c_f32, c_i32, c_i32, c_vp]),
+        "dp_embedding_workspace_size": (size_t, [c_i64] * 3),
+        "dp_embedding_grad": (c_i32, [c_vp] * 3 + [c_i64] * 3 + [c_f32, c_i64, c_i32, c_i32, c_i32, c_vp, c_vp]),
+        "dp_block_norm": (c_i32, [P] + [c_vp] * 12),
+        "dp_block_norm_workspace_size": (size_t, [c_i64] * 2),
+        "dp_block_norm_grad": (c_i32, [P] + [c_vp] * 19),
+        "dp_ckpt8_pitch": (c_i64, [c_i64]),
+        "dp_ckpt8_encode": (c_i32, [c_vp] * 3 + [c_i64] * 3 + [c_i32, c_vp]),
+        "dp_ckpt8_decode": (c_i32, [c_vp] * 3 + [c_i64] * 3 + [c_i32, c_vp]),
+        "dp_act_ckpt8": (c_i32, [c_vp] * 7 + [c_i64] * 4 + [c_i32, c_vp]),
+        "dp_act_ckpt8_grad": (c_i32, [c_vp] * 8 + [c_i64] * 4 + [c_i32, c_vp]),
+        "dp_wgrad8_workspace_size": (size_t, [c_i64] * 3),
+        "dp_wgrad8": (c_i32, [c_vp] * 4 + [c_i64] * 4 + [c_f32, c_i32, c_i32, c_vp, c_vp]),
+    }
+    for name, (res, args) in sig.items():
+        f = getattr(LIB, name)
+        f.restype = res
+        f.argtypes = args
+
+
+_declare()
+
+_DTYPE = {torch.bfloat16: DP_BF16, torch.float32: DP_F32}
+_BF16, _U8, _I8, _F32 = torch.bfloat16, torch.uint8, torch.int8, torch.float32
+
+
+def _dtype(t, name: str) -> int:
+    d = _DTYPE.get(t.dtype)
+    if d is None:
+        raise ValueError("%s: %s is neither bfloat16 nor float32" % (name, t.dtype))
+    return d
+
+
+def _arg(t, shape: Tuple[int, ...], dtype, name: str) -> int:
+    """Address of a contiguous CUDA tensor of this shape and type; None -> NULL."""
+    if t is None:
+        return 0
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s: %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(t, shape: Tuple[int, ...], dtype, name: str) -> Tuple[int, int]:
+    """Address and row stride of a CUDA matrix whose rows are contiguous; None -> (NULL, 0)."""
+    if t is None:
+        return 0, 0
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s: %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    rows, dim = shape
+    if dim > 1 and t.stride(1) != 1:
+        raise ValueError("%s: rows must be contiguous" % name)
+    ld = t.stride(0) if rows > 1 else dim
+    if ld < dim:
+        raise ValueError("%s: rows overlap" % name)
+    return t.data_ptr(), ld
+
+
+def _matrix(t, name: str) -> Tuple[int, int]:
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions" % name)
+    return t.shape
+
+
+def _ws(ws, need: int, name: str = "ws") -> int:
+    if need == 0:
+        return 0 if ws is None else ws.data_ptr()
+    if ws is None:
+        raise ValueError("%s: a workspace of %d bytes is needed" % (name, need))
+    if not ws.is_cuda or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError("%s must be a contiguous CUDA tensor of at least %d bytes" % (name, need))
+    return ws.data_ptr()
+
+
+def _size(n: int, where: str) -> int:
+    if n == 0:
+        raise DPError(DP_ERR_INVALID_ARG, where)
+    return int(n)
+
+
+# ------------------------------------------------------------------------------------------------ embedding lookup
+
+def _ids(ids) -> Tuple[int, int]:
+    if not ids.is_cuda or ids.dim() != 1 or not ids.is_contiguous() or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be a contiguous CUDA vector of int32 or int64")
+    return ids.data_ptr(), 64 if ids.dtype == torch.int64 else 32
+
+
+def dp_embedding(out, table, ids, scale: float = 1.0, stream=None) -> None:
+    """out[t] = scale * table[ids[t]]; a row of zeros where ids[t] is outside [0, vocab)."""
+    (vocab, dim), (pid, bits) = _matrix(table, "table"), _ids(ids)
+    tokens = ids.numel()
+    _check(LIB.dp_embedding(_arg(out, (tokens, dim), table.dtype, "out"), _arg(table, (vocab, dim), table.dtype, "table"),
+                            pid, tokens, vocab, dim, scale, _dtype(table, "table"), bits, _stream(stream)), "dp_embedding")
+
+
+def dp_embedding_workspace_size(tokens: int, vocab: int, dim: int) -> int:
+    return _size(LIB.dp_embedding_workspace_size(tokens, vocab, dim), "dp_embedding_workspace_size")
+
+
+def dp_embedding_grad(dtable, dout, ids, scale: float = 1.0, pad_id: int = -1, accumulate: bool = False, ws=None,
+                      stream=None) -> None:
+    """dtable[v] (+)= scale * the sum of dout[t] over ids[t] = v != pad_id.  ws: dp_embedding_workspace_size bytes."""
+    (vocab, dim), (pid, bits) = _matrix(dtable, "dtable"), _ids(ids)
+    tokens = ids.numel()
+    need = LIB.dp_embedding_workspace_size(tokens, vocab, dim) if tokens else 0
+    _check(LIB.dp_embedding_grad(_arg(dtable, (vocab, dim), dtable.dtype, "dtable"),
+                                 _arg(dout, (tokens, dim), dtable.dtype, "dout"), pid, tokens, vocab, dim, scale, pad_id,
+                                 1 if accumulate else 0, _dtype(dtable, "dtable"), bits, _ws(ws, need), _stream(stream)),
+           "dp_embedding_grad")
+
+
+# -------------------------------------------------------------------------------------------- norms around a block
+
+def _norm_params(x, y, z, params, kind, norms, gate, gate_per_token, res_scale, branch_scale, eps, accumulate):
+    rows, dim = _matrix(x, "x" if z is not None or y is not None else "r")
+    pdt = next((p.dtype for p in params if p is not None), _F32)
+    block = y if y is not None else z
+    bdt = block.dtype if block is not None else x.dtype
+    if pdt not in _DTYPE:
+        raise ValueError("parameters: %s is neither bfloat16 nor float32" % pdt)
+    mode = DP_GATE_NONE if gate is None else DP_GATE_TOKEN if gate_per_token else DP_GATE_CHANNEL
+    p = dp_block_norm_t(rows, dim, kind, norms, mode, _dtype(x, "stream"), _DTYPE.get(bdt, -1), _DTYPE[pdt],
+                        1 if accumulate else 0, eps, res_scale, branch_scale)
+    return p, (rows, dim), bdt, pdt
+
+
+def dp_block_norm(r, z, x, y=None, *, w_post=None, b_post=None, gate=None, gate_per_token: bool = False, w_pre=None,
+                  b_pre=None, post: bool = True, pre: bool = True, kind: int = DP_NORM_RMS, eps: float = 1e-5,
+                  res_scale: float = 1.0, branch_scale: float = 1.0, post_stats=None, pre_stats=None,
+                  stream=None) -> None:
+    """r = res_scale * x + branch_scale * gate * N_post(y), z = N_pre(r).  post=False: N_post(y) is y; pre=False: no z.
+    y=None (and r=None): z = N_pre(x).  post_stats, pre_stats: [rows, 2] float32, (mean, rstd) for the gradient."""
+    params = (w_post, b_post, gate, w_pre, b_pre)
+    norms = (DP_NORM_POST if post and y is not None else 0) | (DP_NORM_PRE if pre else 0)
+    p, shape, bdt, pdt = _norm_params(x, y, z, params, kind, norms, gate, gate_per_token, res_scale, branch_scale, eps, False)
+    rows, dim = shape
+    vec = (dim,)
+    _check(LIB.dp_block_norm(ctypes.byref(p), _arg(r, shape, x.dtype, "r"), _arg(z, shape, bdt, "z"),
+                             _arg(x, shape, x.dtype, "x"), _arg(y, shape, bdt, "y"), _arg(w_post, vec, pdt, "w_post"),
+                             _arg(b_post, vec, pdt, "b_post"), _arg(gate, (rows,) if gate_per_token else vec, pdt, "gate"),
+                             _arg(w_pre, vec, pdt, "w_pre"), _arg(b_pre, vec, pdt, "b_pre"),
+                             _arg(post_stats, (rows, 2), _F32, "post_stats"), _arg(pre_stats, (rows, 2), _F32, "pre_stats"),
+                             _stream(stream)), "dp_block_norm")
+
+
+def dp_block_norm_workspace_size(rows: int, dim: int) -> int:
+    return _size(LIB.dp_block_norm_workspace_size(rows, dim), "dp_block_norm_workspace_size")
+
+
+def dp_block_norm_grad(dx, dy, dr, dz, r, y=None, *, w_post=None, b_post=None, gate=None, gate_per_token: bool = False,
+                       w_pre=None, post: bool = True, pre: bool = True, kind: int = DP_NORM_RMS, res_scale: float = 1.0,
+                       branch_scale: float = 1.0, post_stats=None, pre_stats=None, dw_post=None, db_post=None, dgate=None,
+                       dw_pre=None, db_pre=None, accumulate: bool = False, ws=None, stream=None) -> None:
+    """Gradient of dp_block_norm.  dr: the gradient of r from the rest of the stream (None: zeros); r: the forward's r (x
+    without y); the parameters' gradients are written, or added with accumulate, where they are given.  ws:
+    dp_block_norm_workspace_size bytes."""
+    params = (w_post, b_post, gate, w_pre, dw_post, db_post, dgate, dw_pre, db_pre)
+    norms = (DP_NORM_POST if post and y is not None else 0) | (DP_NORM_PRE if pre else 0)
+    p, shape, bdt, pdt = _norm_params(dx, y, dz, params, kind, norms, gate, gate_per_token, res_scale, branch_scale, 1.0,
+                                      accumulate)
+    rows, dim = shape
+    vec = (dim,)
+    need = LIB.dp_block_norm_workspace_size(rows, dim) if rows else 0
+    gate_shape = (rows,) if gate_per_token else vec
+    _check(LIB.dp_block_norm_grad(
+        ctypes.byref(p), _arg(dx, shape, dx.dtype, "dx"), _arg(dy, shape, bdt, "dy"), _arg(dr, shape, dx.dtype, "dr"),
+        _arg(dz, shape, bdt, "dz"), _arg(r, shape, dx.dtype, "r"), _arg(y, shape, bdt, "y"),
+        _arg(w_post, vec, pdt, "w_post"), _arg(b_post, vec, pdt, "b_post"), _arg(gate, gate_shape, pdt, "gate"),
+        _arg(w_pre, vec, pdt, "w_pre"), _arg(post_stats, (rows, 2), _F32, "post_stats"),
+        _arg(pre_stats, (rows, 2), _F32, "pre_stats"), _arg(dw_post, vec, pdt, "dw_post"),
+        _arg(db_post, vec, pdt, "db_post"), _arg(dgate, gate_shape, pdt, "dgate"), _arg(dw_pre, vec, pdt, "dw_pre"),
+        _arg(db_pre, vec, pdt, "db_pre"), _ws(ws, need), _stream(stream)), "dp_block_norm_grad")
+
+
+# ------------------------------------------------------------------------------------- activation checkpoints in 8 bits
+
+def dp_ckpt8_pitch(dim: int) -> int:
+    """Codes of a row: dim rounded up to whole groups of 32."""
+    if dim < 1:
+        raise ValueError("dim must be at least 1")
+    return -(-dim // DP_CKPT8_GROUP) * DP_CKPT8_GROUP
+
+
+def new_ckpt8(rows: int, dim: int, device=None):
+    """(codes, scales) for a [rows, dim] checkpoint."""
+    pitch, dev = dp_ckpt8_pitch(dim), device or "cuda"
+    return (torch.empty(rows, pitch, dtype=_I8, device=dev),
+            torch.empty(rows, pitch // DP_CKPT8_GROUP, dtype=_U8, device=dev))
+
+
+def _ckpt(codes, scales, rows: int, dim: int, name: str) -> Tuple[int, int]:
+    pitch = -(-dim // DP_CKPT8_GROUP) * DP_CKPT8_GROUP
+    return (_arg(codes, (rows, pitch), _I8, name + " codes"),
+            _arg(scales, (rows, pitch // DP_CKPT8_GROUP), _U8, name + " scales"))
+
+
+def dp_ckpt8_encode(codes, scales, x, stream=None) -> None:
+    """Puts x [rows, dim] (bfloat16 or float32, rows contiguous) away in 8 bits."""
+    rows, dim = _matrix(x, "x")
+    px, ld = _rows(x, (rows, dim), x.dtype, "x")
+    pc, ps = _ckpt(codes, scales, rows, dim, "checkpoint")
+    _check(LIB.dp_ckpt8_encode(pc, ps, px, rows, dim, ld, _dtype(x, "x"), _stream(stream)), "dp_ckpt8_encode")
+
+
+def dp_ckpt8_decode(x, codes, scales, stream=None) -> None:
+    """Writes what the checkpoint stands for to x [rows, dim]."""
+    rows, dim = _matrix(x, "x")
+    px, ld = _rows(x, (rows, dim), x.dtype, "x")
+    pc, ps = _ckpt(codes, scales, rows, dim, "checkpoint")
+    _check(LIB.dp_ckpt8_decode(px, pc, ps, rows, dim, ld, _dtype(x, "x"), _stream(stream)), "dp_ckpt8_decode")
+
+
+def _same_ld(a: int, b: int, what: str, b_given: bool) -> int:
+    if b_given and a != b:
+        raise ValueError("%s must have the same row stride" % what)
+    return a
+
+
+def dp_act_ckpt8(h, g, u=None, *, act: int = DP_ACT_SILU, g8=None, u8=None, stream=None) -> None:
+    """h = f(g) * u (u None: f(g)), and the 8-bit checkpoints g8, u8 -- (codes, scales) pairs -- of g and u.  All bfloat16;
+    g and u may be the two halves of one product (their row strides are the same)."""
+    rows, dim = shape = tuple(_matrix(g, "g"))
+    pg, ld = _rows(g, shape, _BF16, "g")
+    pu, ldu = _rows(u, shape, _BF16, "u")
+    ph, ldh = _rows(h, shape, _BF16, "h")
+    gc, gs = _ckpt(*(g8 or (None, None)), rows, dim, "g8")
+    uc, us = _ckpt(*(u8 or (None, None)), rows, dim, "u8")
+    _check(LIB.dp_act_ckpt8(ph, pg, pu, gc, gs, uc, us, rows, dim, _same_ld(ld, ldu, "g and u", u is not None), ldh, act,
+                            _stream(stream)), "dp_act_ckpt8")
+
+
+def dp_act_ckpt8_grad(dg, du, dh, *, act: int = DP_ACT_SILU, g8=None, u8=None, h=None, stream=None) -> None:
+    """dg and du (None without u8) from dh and the checkpoints; h, where given, receives the activation again."""
+    rows, dim = shape = tuple(_matrix(dh, "dh"))
+    pdg, ld = _rows(dg, shape, _BF16, "dg")
+    pdu, ldu = _rows(du, shape, _BF16, "du")
+    pdh, ldh = _rows(dh, shape, _BF16, "dh")
+    ph, ldo = _rows(h, shape, _BF16, "h")
+    gc, gs = _ckpt(*(g8 or (None, None)), rows, dim, "g8")
+    uc, us = _ckpt(*(u8 or (None, None)), rows, dim, "u8")
+    _check(LIB.dp_act_ckpt8_grad(pdg, pdu, ph, pdh, gc, gs, uc, us, rows, dim,
+                                 _same_ld(ld, ldu, "dg and du", du is not None), _same_ld(ldh, ldo, "dh and h", h is not None),
+                                 act, _stream(stream)), "dp_act_ckpt8_grad")
+
+
+def dp_wgrad8_workspace_size(rows: int, n: int, k: int) -> int:
+    """Bytes of workspace of dp_wgrad8 (0: none is needed)."""
+    return int(LIB.dp_wgrad8_workspace_size(rows, n, k))
+
+
+def dp_wgrad8(dw, dy, codes, scales, alpha: float = 1.0, accumulate: bool = False, ws=None, stream=None) -> None:
+    """dw [n, k] (+)= alpha * dy^T x for dy [rows, n] (bfloat16) and the 8-bit checkpoint of x [rows, k]."""
+    (n, k), (rows, n2) = _matrix(dw, "dw"), _matrix(dy, "dy")
+    py, ld = _rows(dy, (rows, n), _BF16, "dy")
+    pc, ps = _ckpt(codes, scales, rows, k, "checkpoint")
+    need = LIB.dp_wgrad8_workspace_size(rows, n, k)
+    _check(LIB.dp_wgrad8(_arg(dw, (n, k), dw.dtype, "dw"), py, pc, ps, rows, n, k, ld, alpha, 1 if accumulate else 0,
+                         _dtype(dw, "dw"), _ws(ws, need), _stream(stream)), "dp_wgrad8")
