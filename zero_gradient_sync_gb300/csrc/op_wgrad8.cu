@@ -11,8 +11,8 @@
 // a slab of 64 columns x 64 tokens lies as 64 rows of 128 bytes, 128-byte swizzled, which is how TMA writes dy's slabs and
 // how the decoding warps write theirs.
 //
-// Warps of a CTA: 0 loads dy by TMA; 1 (of the first CTA) issues the MMAs; 4-7 read the accumulators out of TMEM and store;
-// 8-15 decode.  The decoders take their codes straight from global memory into registers, a few steps ahead: through
+// Warps of a CTA: 0 loads dy by TMA; 1 (of the first CTA) issues the MMAs; 2 passes complete stages on; 4-7 read the
+// accumulators out of TMEM and store; 8-23 decode.  The decoders take their codes straight from global memory into registers, a few steps ahead: through
 // shared memory they would take a third more of its bandwidth, which is the scarce resource here.  TMEM holds
 // two accumulators, so one tile is stored while the next is multiplied.
 //
@@ -37,10 +37,11 @@ constexpr int STAGES = 6;
 constexpr int SLAB = 64 * 128;                   // 64 tokens x 64 bf16
 constexpr int A_BYTES = 2 * SLAB, B_BYTES = 2 * SLAB, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGING = 32 * 33 * 4;             // a warp's 32 x 32 block of the accumulator
-constexpr int SMEM = STAGES * STAGE_BYTES + 4 * STAGING + 1024 + 256;
-constexpr int THREADS = 512;
-constexpr int EPI0 = 4, DEC0 = 8, DEC_WARPS = 8;
-constexpr int AHEAD = 3;                         // steps of codes in registers
+constexpr int BARS = 8 * (4 * STAGES + 7);
+constexpr int SMEM = STAGES * STAGE_BYTES + 4 * STAGING + 1024 + BARS;
+constexpr int EPI0 = 4, DEC0 = 8, DEC_WARPS = 16;  // first epilogue and decoding warp
+constexpr int THREADS = (DEC0 + DEC_WARPS) * 32;
+constexpr int AHEAD = 4;                         // steps of codes in registers
 constexpr int MAX_SLICES = 32;
 
 struct WgradParams {
@@ -66,23 +67,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // Bounded wait; one that runs out, or that finds the CTA stopping, returns false and leaves the CTA stopping.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* stop) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     for (int i = 0; i < 16; ++i)
-      if (try_wait_cluster(bar, parity)) return true;
+      if (mbar_try_wait(bar, parity)) return true;
     if (*stop) return false;
     if (globaltimer_ns() - t0 > timeout_ns) {
       *stop = 1;
@@ -91,7 +81,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t t
   }
 }
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* stop) {
-  if (try_wait_cluster(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   return wait_slow(bar, parity, timeout_ns, stop);
 }
 // Arrives at the barrier of the same shared-memory offset in CTA `rank` of the cluster.
@@ -99,7 +89,7 @@ __device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
       "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
       : "memory");
 }
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -181,6 +171,31 @@ __device__ __forceinline__ void put_result(const WgradParams& P, int64_t slice, 
   else grad_put(P.dw, row * P.k + col, P.dtype, P.accumulate, v);
 }
 
+// Up to 32 rows of one column of a warp's block to memory.  Adding in fp32 is left to the L2: each element gets one
+// addition a call, so nothing depends on an order, and nobody waits for the old value.  bf16 has to be added in fp32 and
+// rounded once, so its old values are read, 16 rows in flight.
+enum { STORE, ADD };
+template <typename T, int HOW>
+__device__ __forceinline__ void store_rows(T* dst, int64_t ld, const float* block, int rows) {
+  if (HOW == STORE) {
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) dst[r * ld] = Elem<T>::put(block[r * 33]);
+  } else if (sizeof(T) == 4) {
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r)
+      asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(dst + r * ld), "f"(block[r * 33]) : "memory");
+  } else {
+    for (int r0 = 0; r0 < rows; r0 += 16) {
+      T old[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) old[r] = r0 + r < rows ? dst[(r0 + r) * ld] : T(0);
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (r0 + r < rows) dst[(r0 + r) * ld] = Elem<T>::put(__fadd_rn(Elem<T>::get(old[r]), block[(r0 + r) * 33]));
+    }
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     wgrad8_kernel(const __grid_constant__ WgradParams P, const __grid_constant__ CUtensorMap map_dy) {
   extern __shared__ char smem_raw[];
@@ -196,9 +211,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   auto empty = [&](int s) { return bar0 + 8 * (2 * STAGES + s); };
   auto acc_full = [&](int b) { return bar0 + 8 * (3 * STAGES + b); };
   auto acc_empty = [&](int b) { return bar0 + 8 * (3 * STAGES + 2 + b); };
-  const uint32_t drained = bar0 + 8 * (3 * STAGES + 4);
-  volatile int* stop = reinterpret_cast<int*>(bars + 3 * STAGES + 5);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 6);
+  auto decoded = [&](int s) { return bar0 + 8 * (3 * STAGES + 4 + s); };
+  const uint32_t drained = bar0 + 8 * (4 * STAGES + 4);
+  volatile int* stop = reinterpret_cast<int*>(bars + 4 * STAGES + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 6);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -207,7 +223,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(a_full(s), 1);
-      mbar_init(full(s), 2 * DEC_WARPS);
+      mbar_init(decoded(s), DEC_WARPS);
+      mbar_init(full(s), 2);
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -287,6 +304,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         wait_bar(drained, 0, P.timeout_ns, &none);
       }
     }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- stages complete in this CTA -> the pair's MMAs
+    // This warp orders the decoders' writes before the tensor cores' reads and tells the first CTA.  The decoders do not
+    // do so themselves: the fence and the cluster-wide release would wait for the codes that they have in flight.
+    if (lane == 0) {
+      int s = 0, phase = 0;
+      bool ok = true;
+      for (int64_t item = pair; ok && item < P.items; item += pairs) {
+        const int steps = item_at(P, item).steps;
+        for (int i = 0; ok && i < steps; ++i) {
+          ok = (!P.tma || wait_bar(a_full(s), phase, P.timeout_ns, stop)) && wait_bar(decoded(s), phase, P.timeout_ns, stop);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          arrive_at(full(s), 0);
+          if (++s == STAGES) s = 0, phase ^= 1;
+        }
+      }
+    }
   } else if (warp >= EPI0 && warp < EPI0 + 4) {
     // ---------------------------------------------------------------- accumulators to memory
     const int quad = warp - EPI0;  // TMEM lanes 32 quad .. + 31: this warp may read no others
@@ -297,21 +332,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!wait_bar(acc_full(b), bphase, P.timeout_ns, stop)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int64_t row0 = it.row0 + rank * 128 + quad * 32;
+      const int rows = (int)(row0 >= P.n ? 0 : P.n - row0 < 32 ? P.n - row0 : 32);
       for (int c = 0; c < BN; c += 32) {
-        const int64_t col = it.col0 + c + lane;
         uint32_t v[32];
-        __syncwarp();
         tmem_load32(tmem + ((uint32_t)quad << 21) + b * BN + c, v);
+        __syncwarp();  // the previous block has been read
 #pragma unroll
         for (int i = 0; i < 32; ++i) mine[lane * 33 + i] = __uint_as_float(v[i]) * P.alpha;
         __syncwarp();
         // Row by row: 32 lanes, 32 consecutive columns.
-        if (row0 < P.n && it.col0 + c < P.k) {
-          const int rows = (int)(P.n - row0 < 32 ? P.n - row0 : 32);
-          if (col < P.k) {
-#pragma unroll 8
-            for (int r = 0; r < rows; ++r) put_result(P, it.slice, row0 + r, col, mine[r * 33 + lane]);
-          }
+        const int64_t col = it.col0 + c + lane;
+        if (col >= P.k) continue;
+        if (P.part) store_rows<float, STORE>(P.part + (it.slice * P.n + row0) * P.k + col, P.k, mine + lane, rows);
+        else if (P.dtype == DP_F32) {
+          float* dst = static_cast<float*>(P.dw) + row0 * P.k + col;
+          if (P.accumulate) store_rows<float, ADD>(dst, P.k, mine + lane, rows);
+          else store_rows<float, STORE>(dst, P.k, mine + lane, rows);
+        } else {
+          bf16_t* dst = static_cast<bf16_t*>(P.dw) + row0 * P.k + col;
+          if (P.accumulate) store_rows<bf16_t, ADD>(dst, P.k, mine + lane, rows);
+          else store_rows<bf16_t, STORE>(dst, P.k, mine + lane, rows);
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -321,42 +361,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= DEC0) {
     // ---------------------------------------------------------------- codes to bf16 tiles
-    // A thread decodes one group of 32 codes of one token a step: 8 tokens x 4 groups a warp.
+    // A thread decodes half a group, 16 codes of one token, a step: 4 tokens x 8 halves a warp.
     const int t = threadIdx.x - DEC0 * 32;
-    const int token = t >> 2, q = t & 3;
+    const int token = t >> 3, h = t & 7;
     const int64_t groups = P.pitch / DP_CKPT8_GROUP;
-    uint4 c0[AHEAD], c1[AHEAD];
+    uint4 c[AHEAD];
     uint32_t E[AHEAD];
     // The loading side runs AHEAD steps before the decoding side.
-    int64_t litem = pair;
-    Item lit = {};
-    int li = 0;
-    if (litem < P.items) lit = item_at(P, litem);
-    auto load = [&](uint4& x, uint4& y, uint32_t& e) {
-      if (litem >= P.items) return;
-      const int64_t m = lit.token0 + (int64_t)li * BK + token, col = lit.col0 + rank * 128 + q * 32;
-      x = y = make_uint4(0, 0, 0, 0);
-      e = 1;
-      if (m < P.rows && col < P.pitch) {
-        const uint4* src = reinterpret_cast<const uint4*>(P.codes + m * P.pitch + col);
-        x = __ldg(src);
-        y = __ldg(src + 1);
-        e = P.scales[m * groups + col / DP_CKPT8_GROUP];
-      }
-      if (++li == lit.steps) {
-        li = 0;
+    int64_t litem = pair, left = 0;  // tokens from this thread's to the end
+    int lsteps = 0;
+    bool inside = false;             // its columns exist
+    const int8_t* code_at = nullptr;
+    const uint8_t* scale_at = nullptr;
+    auto load = [&](uint4& x, uint32_t& e) {
+      if (lsteps == 0) {
+        if (litem >= P.items) return;
+        const Item it = item_at(P, litem);
         litem += pairs;
-        if (litem < P.items) lit = item_at(P, litem);
+        lsteps = it.steps;
+        const int64_t m = it.token0 + token, col = it.col0 + rank * 128 + h * 16;
+        left = P.rows - m;
+        inside = col < P.pitch;
+        code_at = P.codes + m * P.pitch + col;
+        scale_at = P.scales + m * groups + col / DP_CKPT8_GROUP;
       }
+      x = make_uint4(0, 0, 0, 0);
+      e = 1;
+      if (inside && left > 0) {
+        x = __ldg(reinterpret_cast<const uint4*>(code_at));
+        e = __ldg(scale_at);
+      }
+      left -= BK;
+      code_at += BK * P.pitch;
+      scale_at += BK * groups;
+      --lsteps;
     };
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) load(c0[u], c1[u], E[u]);
-    // Where the thread's four 16-byte pieces go: slab q / 2, row `token`, piece p at place p ^ (token mod 8).  Threads
-    // of the second slab take their pieces in another order, so that eight neighbours hit all banks.
-    const uint32_t line = (uint32_t)(A_BYTES + (q >> 1) * SLAB + token * 128);
-    const uint32_t sw = (uint32_t)(token & 7);
-    const uint32_t p0 = (uint32_t)(q & 1) * 4;
-    const uint32_t turn = (uint32_t)(q >> 1) * 2;
+    for (int u = 0; u < AHEAD; ++u) load(c[u], E[u]);
+    // Where the thread's two 16-byte pieces go: slab h / 4, row `token`, piece p at place p ^ (token mod 8).  Threads of the
+    // second slab store their second piece first, so that the eight of a token hit all banks.
+    const uint32_t line = (uint32_t)(A_BYTES + (h >> 2) * SLAB + token * 128);
+    const uint32_t turn = (uint32_t)(h >> 2);
+    const uint32_t at0 = line + ((((uint32_t)(h & 3) * 2 + turn) ^ (uint32_t)(token & 7)) << 4);
+    const uint32_t at1 = at0 ^ 16;
     int s = 0, phase = 0;
     int64_t item = pair;
     Item it = {};
@@ -367,26 +414,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
         if (!ok || item >= P.items) break;
-        ok = wait_bar(empty(s), phase ^ 1, P.timeout_ns, stop);
-        if (!ok) break;
         const uint16_t sb = E[u] == 255u ? (uint16_t)0x7fc0u : (uint16_t)(E[u] << 7);
         const __nv_bfloat162 step = __bfloat162bfloat162(*reinterpret_cast<const __nv_bfloat16*>(&sb));
+        const uint2 a0 = decode4(turn ? c[u].z : c[u].x, step), a1 = decode4(turn ? c[u].w : c[u].y, step);
+        const uint2 b0 = decode4(turn ? c[u].x : c[u].z, step), b1 = decode4(turn ? c[u].y : c[u].w, step);
+        ok = wait_bar(empty(s), phase ^ 1, P.timeout_ns, stop);
+        if (!ok) break;
         char* stage = smem + s * STAGE_BYTES;
-        const uint32_t w[8] = {c0[u].x, c0[u].y, c0[u].z, c0[u].w, c1[u].x, c1[u].y, c1[u].z, c1[u].w};
-        uint4 o[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const uint2 lo = decode4(w[2 * p], step), hi = decode4(w[2 * p + 1], step);
-          o[p] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        }
-        if (turn) {
-          uint4 x = o[0]; o[0] = o[2]; o[2] = x;
-          x = o[1]; o[1] = o[3]; o[3] = x;
-        }
-#pragma unroll
-        for (uint32_t p = 0; p < 4; ++p)
-          *reinterpret_cast<uint4*>(stage + line + (((p0 + (p ^ turn)) ^ sw) << 4)) = o[p];
-        load(c0[u], c1[u], E[u]);
+        *reinterpret_cast<uint4*>(stage + at0) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+        *reinterpret_cast<uint4*>(stage + at1) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+        load(c[u], E[u]);
         if (!P.tma) {
           // dy's rows are not 16-byte aligned: the decoders copy its tile too, one element at a time.
           const int64_t m0 = it.token0 + (int64_t)i * BK;
@@ -400,12 +437,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                          (col & 7) * 2) = v;
           }
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          const bool here = !P.tma || wait_bar(a_full(s), phase, P.timeout_ns, stop);
-          if (here) arrive_at(full(s), 0);
-        }
+        if (lane == 0) mbar_arrive(decoded(s));
         if (++s == STAGES) s = 0, phase ^= 1;
         if (++i == it.steps) {
           i = 0;
