@@ -119,7 +119,7 @@ dp_status_t dp_block_norm_grad(const dp_block_norm_t* p, void* dx, void* dy, con
  * E = 1 for a group of zeros.  A group that holds an infinity or a NaN has
  * E = 255 and stands for NaNs, so that an overflow reaches the gradients and
  * skips the step.  A code times its step has at most 7 bits: the value is exact
- * in bf16.  codes: [rows][pitch] int8, 16-byte aligned; scales: [rows][pitch /
+ * in bf16.  codes: [rows][pitch] int8, 32-byte aligned; scales: [rows][pitch /
  * 32] bytes. */
 enum { DP_CKPT8_GROUP = 32 };
 int64_t dp_ckpt8_pitch(int64_t dim); /* dim rounded up to a multiple of 32; -1 if dim < 1 */

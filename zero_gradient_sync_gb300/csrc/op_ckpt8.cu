@@ -220,7 +220,7 @@ dp_status_t check_ld(int64_t ld, int64_t dim, const char* name) {
 }
 dp_status_t check_ckpt(const int8_t* codes, const uint8_t* scales, bool needed, const char* name) {
   if ((!codes || !scales) && needed) return op_fail(DP_ERR_INVALID_ARG, "%s: codes or scales are NULL", name);
-  if (!is_aligned(codes, 16)) return op_fail(DP_ERR_ALIGNMENT, "%s: codes are not 16-byte aligned", name);
+  if (!is_aligned(codes, 32)) return op_fail(DP_ERR_ALIGNMENT, "%s: codes are not 32-byte aligned", name);
   return DP_OK;
 }
 Walk walk_of(int64_t rows, int64_t dim) { return Walk{rows, (int)(dp_ckpt8_pitch(dim) / 8), (int)dim}; }

@@ -11,10 +11,14 @@
 // a slab of 64 columns x 64 tokens lies as 64 rows of 128 bytes, 128-byte swizzled, which is how TMA writes dy's slabs and
 // how the decoding warps write theirs.
 //
-// Warps of a CTA: 0 loads dy by TMA; 1 (of the first CTA) issues the MMAs; 2 passes complete stages on; 4-7 read the
-// accumulators out of TMEM and store; 8-23 decode.  The decoders take their codes straight from global memory into registers, a few steps ahead: through
-// shared memory they would take a third more of its bandwidth, which is the scarce resource here.  TMEM holds
-// two accumulators, so one tile is stored while the next is multiplied.
+// Warps of a CTA: 0 loads dy by TMA; 1 (of the first CTA) issues the MMAs; 2 passes complete stages on; 4-11 take the
+// accumulators out of TMEM; 12-19 decode.  The decoders load their codes straight from global memory into registers, three
+// steps ahead: through shared memory they would take a quarter more of its bandwidth.
+//
+// Sums: the tensor cores cut the sums that they accumulate in TMEM rather than round them, so the error of a long sum grows with
+// its length (5.7e-6 of the result's norm after 8192 tokens, where fp32 rounded at every step gives 5.4e-7).  So every
+// 512 tokens start a new accumulator, and the finished one is added, rounded, to sums that eight warps hold in registers
+// (128 a thread: setmaxnreg gives them what the other warps do without).  TMEM holds two accumulators, so the MMAs go on.
 //
 // Decoding: with b = code bits, 0x4300 | (b & 0x7f) is the bf16 128 + (b & 0x7f), and 0x4300 | (b & 0x80) is 128, or 256 for a
 // negative code; their difference is the code, exactly, and times a power of two it stays exact: five instructions for two
@@ -36,12 +40,16 @@ constexpr int BM = 256, BN = 256, BK = 64;       // dw rows, dw columns, tokens 
 constexpr int STAGES = 6;
 constexpr int SLAB = 64 * 128;                   // 64 tokens x 64 bf16
 constexpr int A_BYTES = 2 * SLAB, B_BYTES = 2 * SLAB, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int STAGING = 32 * 33 * 4;             // a warp's 32 x 32 block of the accumulator
-constexpr int BARS = 8 * (4 * STAGES + 7);
-constexpr int SMEM = STAGES * STAGE_BYTES + 4 * STAGING + 1024 + BARS;
-constexpr int EPI0 = 4, DEC0 = 8, DEC_WARPS = 16;  // first epilogue and decoding warp
+constexpr int STAGING = 32 * 33 * 4;             // a warp's 32 x 32 block of the result
+constexpr int CHUNK = 8;                         // steps of one accumulator
+constexpr int EPI0 = 4, EPI_WARPS = 8, DEC0 = 12, DEC_WARPS = 8;
 constexpr int THREADS = (DEC0 + DEC_WARPS) * 32;
-constexpr int AHEAD = 4;                         // steps of codes in registers
+constexpr int AHEAD = 3;                         // steps of codes in registers; divides STAGES
+// Registers a thread: 96 at launch (640 threads); control warps give up 48, decoders 40, summing warps take 64: 48 + 2 * 160
+// + 2 * 56 = 5 * 96.
+constexpr int REGS_CONTROL = 48, REGS_SUM = 160, REGS_DECODE = 56;
+constexpr int BARS = 8 * (4 * STAGES + 7);
+constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * STAGING + 1024 + BARS;
 constexpr int MAX_SLICES = 32;
 
 struct WgradParams {
@@ -53,7 +61,7 @@ struct WgradParams {
   int64_t rows, n, k, lddy, pitch;
   int64_t tiles_k, tiles, items, steps;  // steps: of 64 tokens, of one slice
   float alpha;
-  int dtype, accumulate, tma;
+  int dtype, accumulate;
   uint64_t timeout_ns;
 };
 
@@ -68,7 +76,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Bounded wait; one that runs out, or that finds the CTA stopping, returns false and leaves the CTA stopping.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* stop) {
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* stop) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     for (int i = 0; i < 16; ++i)
@@ -120,17 +128,20 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(addr)
       : "memory");
+}
+// 32 bytes of codes, 32-byte aligned.
+__device__ __forceinline__ void load_codes(const int8_t* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
 }
 
 // Two bf16 values of two codes already spread over bytes 0 and 2: lo7 = 0x43 mm 0x43 mm, sign = 0x43 ss 0x43 ss.
@@ -173,29 +184,34 @@ __device__ __forceinline__ void put_result(const WgradParams& P, int64_t slice, 
 
 // Up to 32 rows of one column of a warp's block to memory.  Adding in fp32 is left to the L2: each element gets one
 // addition a call, so nothing depends on an order, and nobody waits for the old value.  bf16 has to be added in fp32 and
-// rounded once, so its old values are read, 16 rows in flight.
-enum { STORE, ADD };
-template <typename T, int HOW>
-__device__ __forceinline__ void store_rows(T* dst, int64_t ld, const float* block, int rows) {
-  if (HOW == STORE) {
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r) dst[r * ld] = Elem<T>::put(block[r * 33]);
-  } else if (sizeof(T) == 4) {
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r)
-      asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(dst + r * ld), "f"(block[r * 33]) : "memory");
-  } else {
-    for (int r0 = 0; r0 < rows; r0 += 16) {
-      T old[16];
+// rounded once, so its old values are read, 8 rows in flight.
+__device__ __forceinline__ void store_block(const WgradParams& P, int64_t slice, int64_t row0, int64_t col, const float* block,
+                                            int rows) {
+  if (!P.part && P.dtype == DP_BF16) {
+    bf16_t* dst = static_cast<bf16_t*>(P.dw) + row0 * P.k + col;
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      float old[8];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) old[r] = r0 + r < rows ? dst[(r0 + r) * ld] : T(0);
+      for (int r = 0; r < 8; ++r) old[r] = P.accumulate && r0 + r < rows ? bf16_to_f32(dst[r * P.k]) : 0.0f;
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (r0 + r < rows) dst[(r0 + r) * ld] = Elem<T>::put(__fadd_rn(Elem<T>::get(old[r]), block[(r0 + r) * 33]));
+      for (int r = 0; r < 8; ++r)
+        if (r0 + r < rows) dst[r * P.k] = bf16_rn(__fadd_rn(old[r], block[(r0 + r) * 33]));
+      dst += 8 * P.k;
     }
+    return;
+  }
+  float* dst = (P.part ? P.part + slice * P.n * P.k : static_cast<float*>(P.dw)) + row0 * P.k + col;
+  const bool add = !P.part && P.accumulate;
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r) {
+    const float v = block[r * 33];
+    if (add) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(dst), "f"(v) : "memory");
+    else *dst = v;
+    dst += P.k;
   }
 }
 
+template <bool TMA>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     wgrad8_kernel(const __grid_constant__ WgradParams P, const __grid_constant__ CUtensorMap map_dy) {
   extern __shared__ char smem_raw[];
@@ -204,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   char* smem = smem_raw + (tiles - smem0);
   char* after = smem + STAGES * STAGE_BYTES;
   float* staging = reinterpret_cast<float*>(after);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(after + 4 * STAGING);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(after + EPI_WARPS * STAGING);
   const uint32_t bar0 = smem_u32(bars);
   auto a_full = [&](int s) { return bar0 + 8 * s; };
   auto full = [&](int s) { return bar0 + 8 * (STAGES + s); };
@@ -229,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 2 * 4);
+      mbar_init(acc_empty(b), 2 * EPI_WARPS);
     }
     mbar_init(drained, 1);
     *stop = 0;
@@ -245,9 +261,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
+  if (warp < EPI0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONTROL));
   if (warp == 0) {
     // ---------------------------------------------------------------- dy by TMA: two slabs of 64 columns a step
-    if (lane == 0 && P.tma) {
+    if (TMA && lane == 0) {
       int s = 0, phase = 0;
       int64_t issued = 0;
       bool ok = true;
@@ -279,24 +296,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       for (int64_t item = pair; ok && item < P.items; item += pairs) {
         const Item it = item_at(P, item);
-        ok = wait_bar(acc_empty(b), bphase ^ 1, P.timeout_ns, stop);
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + b * BN;
         for (int i = 0; i < it.steps; ++i) {
-          ok = wait_bar(full(s), phase, P.timeout_ns, stop);
+          const bool fresh = i % CHUNK == 0;
+          ok = (!fresh || wait_bar(acc_empty(b), bphase ^ 1, P.timeout_ns, stop)) && wait_bar(full(s), phase, P.timeout_ns, stop);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t a = tiles + s * STAGE_BYTES;
 #pragma unroll
           for (int q = 0; q < BK / 16; ++q)  // 16 tokens: two groups of eight, 2048 bytes on
-            mma_pair(d, operand_desc(a + q * 2048), operand_desc(a + A_BYTES + q * 2048), (i | q) != 0);
+            mma_pair(tmem + b * BN, operand_desc(a + q * 2048), operand_desc(a + A_BYTES + q * 2048), !fresh || q != 0);
           commit_pair(empty(s));
           if (++s == STAGES) s = 0, phase ^= 1;
+          if (i % CHUNK == CHUNK - 1 || i == it.steps - 1) {
+            commit_pair(acc_full(b));
+            if (++b == 2) b = 0, bphase ^= 1;
+          }
         }
-        if (!ok) break;
-        commit_pair(acc_full(b));
-        if (++b == 2) b = 0, bphase ^= 1;
       }
       if (!ok) {  // MMAs in flight end before the CTA may end
         volatile int none = 0;
@@ -314,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int64_t item = pair; ok && item < P.items; item += pairs) {
         const int steps = item_at(P, item).steps;
         for (int i = 0; ok && i < steps; ++i) {
-          ok = (!P.tma || wait_bar(a_full(s), phase, P.timeout_ns, stop)) && wait_bar(decoded(s), phase, P.timeout_ns, stop);
+          ok = (!TMA || wait_bar(a_full(s), phase, P.timeout_ns, stop)) && wait_bar(decoded(s), phase, P.timeout_ns, stop);
           if (!ok) break;
           fence_proxy_async_smem();
           arrive_at(full(s), 0);
@@ -322,112 +337,127 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
     }
-  } else if (warp >= EPI0 && warp < EPI0 + 4) {
-    // ---------------------------------------------------------------- accumulators to memory
-    const int quad = warp - EPI0;  // TMEM lanes 32 quad .. + 31: this warp may read no others
-    float* mine = staging + quad * (32 * 33);
+  } else if (warp >= EPI0 && warp < DEC0) {
+    // ---------------------------------------------------------------- sums, and the result to memory
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SUM));
+    const int quad = warp & 3;               // TMEM lanes 32 quad .. + 31: a warp may read no others
+    const int half = (warp - EPI0) >> 2;     // columns 128 half .. + 127
+    float* mine = staging + (warp - EPI0) * (32 * 33);
+    const uint32_t from = tmem + ((uint32_t)quad << 21) + half * 128;
     int b = 0, bphase = 0;
-    for (int64_t item = pair; item < P.items; item += pairs) {
+    bool ok = true;
+    for (int64_t item = pair; ok && item < P.items; item += pairs) {
+      float sum[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) sum[i] = 0.0f;
+      for (int left = item_at(P, item).steps; left > 0; left -= CHUNK) {
+        ok = wait_bar(acc_full(b), bphase, P.timeout_ns, stop);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          uint32_t v[16];
+          tmem_load16(from + b * BN + c, v);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) sum[c + q] = __fadd_rn(sum[c + q], __uint_as_float(v[q]));
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive_at(acc_empty(b), 0);
+        if (++b == 2) b = 0, bphase ^= 1;
+      }
+      if (!ok) break;
       const Item it = item_at(P, item);
-      if (!wait_bar(acc_full(b), bphase, P.timeout_ns, stop)) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int64_t row0 = it.row0 + rank * 128 + quad * 32;
       const int rows = (int)(row0 >= P.n ? 0 : P.n - row0 < 32 ? P.n - row0 : 32);
-      for (int c = 0; c < BN; c += 32) {
-        uint32_t v[32];
-        tmem_load32(tmem + ((uint32_t)quad << 21) + b * BN + c, v);
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
         __syncwarp();  // the previous block has been read
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mine[lane * 33 + i] = __uint_as_float(v[i]) * P.alpha;
+        for (int i = 0; i < 32; ++i) mine[lane * 33 + i] = sum[c + i] * P.alpha;
         __syncwarp();
         // Row by row: 32 lanes, 32 consecutive columns.
-        const int64_t col = it.col0 + c + lane;
-        if (col >= P.k) continue;
-        if (P.part) store_rows<float, STORE>(P.part + (it.slice * P.n + row0) * P.k + col, P.k, mine + lane, rows);
-        else if (P.dtype == DP_F32) {
-          float* dst = static_cast<float*>(P.dw) + row0 * P.k + col;
-          if (P.accumulate) store_rows<float, ADD>(dst, P.k, mine + lane, rows);
-          else store_rows<float, STORE>(dst, P.k, mine + lane, rows);
-        } else {
-          bf16_t* dst = static_cast<bf16_t*>(P.dw) + row0 * P.k + col;
-          if (P.accumulate) store_rows<bf16_t, ADD>(dst, P.k, mine + lane, rows);
-          else store_rows<bf16_t, STORE>(dst, P.k, mine + lane, rows);
-        }
+        const int64_t col = it.col0 + half * 128 + c + lane;
+        if (col < P.k) store_block(P, it.slice, row0, col, mine + lane, rows);
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) arrive_at(acc_empty(b), 0);
-      if (++b == 2) b = 0, bphase ^= 1;
     }
   } else if (warp >= DEC0) {
     // ---------------------------------------------------------------- codes to bf16 tiles
-    // A thread decodes half a group, 16 codes of one token, a step: 4 tokens x 8 halves a warp.
+    // A thread decodes one group of 32 codes of one token a step; a warp 8 tokens x 4 groups.  Eight neighbours, whose
+    // 16-byte stores go together, hold 4 tokens x 2 groups of one slab: the swizzle puts these into 8 different places.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DECODE));
     const int t = threadIdx.x - DEC0 * 32;
-    const int token = t >> 3, h = t & 7;
-    const int64_t groups = P.pitch / DP_CKPT8_GROUP;
-    uint4 c[AHEAD];
+    const int token = (t >> 5) * 8 + ((t >> 4) & 1) * 4 + ((t >> 1) & 3), q = ((t >> 3) & 1) * 2 + (t & 1);
+    uint32_t c[AHEAD][8];
     uint32_t E[AHEAD];
-    // The loading side runs AHEAD steps before the decoding side.
-    int64_t litem = pair, left = 0;  // tokens from this thread's to the end
-    int lsteps = 0;
-    bool inside = false;             // its columns exist
+    // The loading side runs AHEAD steps before the decoding side.  Where a token or a group is beyond the end, the step 0
+    // makes zeros of whatever codes the registers hold.
+    int64_t litem = pair;
+    int lsteps = 0, lvalid = 0;      // steps of the item, and of them this thread's, still to load
     const int8_t* code_at = nullptr;
     const uint8_t* scale_at = nullptr;
-    auto load = [&](uint4& x, uint32_t& e) {
+    const int64_t code_step = BK * P.pitch, scale_step = BK * (P.pitch / DP_CKPT8_GROUP);
+    auto load = [&](uint32_t (&w)[8], uint32_t& e) {
       if (lsteps == 0) {
         if (litem >= P.items) return;
         const Item it = item_at(P, litem);
         litem += pairs;
         lsteps = it.steps;
-        const int64_t m = it.token0 + token, col = it.col0 + rank * 128 + h * 16;
-        left = P.rows - m;
-        inside = col < P.pitch;
+        const int64_t m = it.token0 + token, col = it.col0 + rank * 128 + q * 32;
+        const int64_t valid = col < P.pitch && m < P.rows ? (P.rows - m + BK - 1) / BK : 0;
+        lvalid = (int)(valid < lsteps ? valid : lsteps);
         code_at = P.codes + m * P.pitch + col;
-        scale_at = P.scales + m * groups + col / DP_CKPT8_GROUP;
+        scale_at = P.scales + m * (P.pitch / DP_CKPT8_GROUP) + col / DP_CKPT8_GROUP;
       }
-      x = make_uint4(0, 0, 0, 0);
-      e = 1;
-      if (inside && left > 0) {
-        x = __ldg(reinterpret_cast<const uint4*>(code_at));
+      e = 0;
+      if (lvalid > 0) {
+        load_codes(code_at, w);
         e = __ldg(scale_at);
       }
-      left -= BK;
-      code_at += BK * P.pitch;
-      scale_at += BK * groups;
+      code_at += code_step;
+      scale_at += scale_step;
+      --lvalid;
       --lsteps;
     };
+    int64_t total = 0;
+    for (int64_t item = pair; item < P.items; item += pairs) total += item_at(P, item).steps;
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) load(c[u], E[u]);
-    // Where the thread's two 16-byte pieces go: slab h / 4, row `token`, piece p at place p ^ (token mod 8).  Threads of the
-    // second slab store their second piece first, so that the eight of a token hit all banks.
-    const uint32_t line = (uint32_t)(A_BYTES + (h >> 2) * SLAB + token * 128);
-    const uint32_t turn = (uint32_t)(h >> 2);
-    const uint32_t at0 = line + ((((uint32_t)(h & 3) * 2 + turn) ^ (uint32_t)(token & 7)) << 4);
-    const uint32_t at1 = at0 ^ 16;
-    int s = 0, phase = 0;
-    int64_t item = pair;
-    Item it = {};
-    if (item < P.items) it = item_at(P, item);
-    int i = 0;
+    for (int u = 0; u < AHEAD; ++u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[u][i] = 0;
+      E[u] = 0;
+      load(c[u], E[u]);
+    }
+    // The thread's four 16-byte pieces: slab q / 2, row `token`, piece p at place p ^ (token mod 8).
+    char* line = smem + A_BYTES + (q >> 1) * SLAB + token * 128;
+    const uint32_t first = ((uint32_t)(q & 1) * 4 ^ (uint32_t)(token & 7)) << 4;
+    int64_t citem = pair;            // (without TMA) the item and step whose dy is copied
+    int ci = 0;
+    uint32_t phase = 1;
     bool ok = true;
-    while (ok && item < P.items) {
+    for (int64_t done = 0; ok && done < total; done += STAGES, phase ^= 1) {
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        if (!ok || item >= P.items) break;
-        const uint16_t sb = E[u] == 255u ? (uint16_t)0x7fc0u : (uint16_t)(E[u] << 7);
-        const __nv_bfloat162 step = __bfloat162bfloat162(*reinterpret_cast<const __nv_bfloat16*>(&sb));
-        const uint2 a0 = decode4(turn ? c[u].z : c[u].x, step), a1 = decode4(turn ? c[u].w : c[u].y, step);
-        const uint2 b0 = decode4(turn ? c[u].x : c[u].z, step), b1 = decode4(turn ? c[u].y : c[u].w, step);
-        ok = wait_bar(empty(s), phase ^ 1, P.timeout_ns, stop);
+      for (int s = 0; s < STAGES; ++s) {
+        if (done + s >= total) break;
+        const int u = s % AHEAD;
+        // A step byte is a bf16's exponent.  255, an infinity, makes NaNs of the zero codes of such a group.
+        const uint32_t sb = __byte_perm(E[u] << 7, 0, 0x1010);
+        const __nv_bfloat162 step = *reinterpret_cast<const __nv_bfloat162*>(&sb);
+        ok = wait_bar(empty(s), phase, P.timeout_ns, stop);
         if (!ok) break;
-        char* stage = smem + s * STAGE_BYTES;
-        *reinterpret_cast<uint4*>(stage + at0) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-        *reinterpret_cast<uint4*>(stage + at1) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+        char* to = line + s * STAGE_BYTES;
+#pragma unroll
+        for (uint32_t p = 0; p < 4; ++p) {
+          const uint2 lo = decode4(c[u][2 * p], step), hi = decode4(c[u][2 * p + 1], step);
+          *reinterpret_cast<uint4*>(to + (first ^ (p << 4))) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
         load(c[u], E[u]);
-        if (!P.tma) {
+        if (!TMA) {
           // dy's rows are not 16-byte aligned: the decoders copy its tile too, one element at a time.
-          const int64_t m0 = it.token0 + (int64_t)i * BK;
-          const int64_t n0 = it.row0 + rank * 128;
+          const Item it = item_at(P, citem);
+          const int64_t m0 = it.token0 + (int64_t)ci * BK, n0 = it.row0 + rank * 128;
+          char* stage = smem + s * STAGE_BYTES;
 #pragma unroll 4
           for (int e = t; e < BK * 128; e += DEC_WARPS * 32) {
             const int tok = e >> 7, col = e & 127;
@@ -436,15 +466,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             *reinterpret_cast<uint16_t*>(stage + (col >> 6) * SLAB + tok * 128 + ((((col & 63) >> 3) ^ (tok & 7)) << 4) +
                                          (col & 7) * 2) = v;
           }
+          if (++ci == it.steps) ci = 0, citem += pairs;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(decoded(s));
-        if (++s == STAGES) s = 0, phase ^= 1;
-        if (++i == it.steps) {
-          i = 0;
-          item += pairs;
-          if (item < P.items) it = item_at(P, item);
-        }
       }
     }
   }
@@ -545,7 +570,7 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
   DP_TRY(check_dev(dw, elem_size(dtype), true, "dw"));
   DP_TRY(check_dev(dy, 2, rows > 0, "dy"));
   if (rows > 0 && (!codes || !scales)) return op_fail(DP_ERR_INVALID_ARG, "codes or scales are NULL");
-  if (!is_aligned(codes, 16)) return op_fail(DP_ERR_ALIGNMENT, "codes are not 16-byte aligned");
+  if (!is_aligned(codes, 32)) return op_fail(DP_ERR_ALIGNMENT, "codes are not 32-byte aligned");
   const Split s = split_of(rows, n, k);
   DP_TRY(check_dev(ws, 256, s.slices > 1, "ws"));
   const cudaStream_t stream = (cudaStream_t)stream_;
@@ -575,9 +600,9 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
   P.accumulate = accumulate;
   P.timeout_ns = dp_get_wait_timeout_ns();
   // TMA wants 16-byte aligned rows; other rows are copied by the decoding warps.
-  P.tma = is_aligned(dy, 16) && lddy % 8 == 0;
+  const bool tma = is_aligned(dy, 16) && lddy % 8 == 0;
   CUtensorMap map = {};
-  if (P.tma) {
+  if (tma) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return op_fail(DP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint64_t dims[2] = {(cuuint64_t)n, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)lddy * 2};
@@ -587,10 +612,11 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return op_fail(DP_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
   }
-  const cudaError_t attr = cudaFuncSetAttribute(wgrad8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  auto kernel = tma ? wgrad8_kernel<true> : wgrad8_kernel<false>;
+  const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (attr != cudaSuccess) return op_fail(DP_ERR_CUDA, "weight gradient: %s", cudaGetErrorString(attr));
   const int64_t pairs = sm_count() / 2;
-  wgrad8_kernel<<<(unsigned)(2 * (P.items < pairs ? P.items : pairs)), THREADS, SMEM, stream>>>(P, map);
+  kernel<<<(unsigned)(2 * (P.items < pairs ? P.items : pairs)), THREADS, SMEM, stream>>>(P, map);
   if (!P.part) return op_launched("weight gradient launch", 1);
   const int64_t size = n * k, ctas = (size + 1023) / 1024, most = (int64_t)sm_count() * 8;
   wgrad8_join_kernel<<<(unsigned)(ctas < most ? ctas : most), 256, 0, stream>>>(P.part, dw, size, (int)s.slices, dtype,
