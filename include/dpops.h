@@ -149,14 +149,19 @@ dp_status_t dp_act_ckpt8_grad(uint16_t* dg, uint16_t* du, uint16_t* h, const uin
                               const uint8_t* g8_scales, const int8_t* u8, const uint8_t* u8_scales, int64_t rows,
                               int64_t dim, int64_t ld, int64_t ldh, int32_t act, dp_stream_t stream);
 
-/* Bytes of workspace of dp_wgrad8; 0 on a bad size (and where none is needed). */
-size_t dp_wgrad8_workspace_size(int64_t rows, int64_t n, int64_t k);
+/* Bytes of workspace of dp_wgrad8: x decoded (2 bytes a value), the products of
+ * tiles split over the rows, and, where n is no multiple of 8 or dy_aligned is 0,
+ * a copy of dy.  dy_aligned: dy's rows are 16-byte aligned where n is a
+ * multiple of 8.  0 on a bad size. */
+size_t dp_wgrad8_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dy_aligned);
 
 /* Weight gradient of y = x W^T from the 8-bit checkpoint of x (write or add):
  *   dw[i][j] (+)= alpha * sum over the rows m of dy[m][i] * x[m][j]
  * dy: bf16 [rows][n], row stride lddy; codes, scales: the checkpoint of x
  * [rows][k]; dw: [n][k], contiguous, `dtype`.  dy and the decoded x (both exact
- * in bf16) are multiplied on the tensor cores and summed in fp32. */
+ * in bf16) are multiplied on the tensor cores and summed in fp32.  A wait that
+ * runs out in the kernel (dp_set_wait_timeout_ns) leaves NaNs in dw, which skip
+ * the step. */
 dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t n,
                       int64_t k, int64_t lddy, float alpha, int32_t accumulate, int32_t dtype, void* ws,
                       dp_stream_t stream);

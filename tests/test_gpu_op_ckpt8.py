@@ -155,7 +155,7 @@ def test_overflow_reaches_the_gradients(dev):
     assert nan[2, 32:].all() and int(nan.sum()) == 32
     dy = torch.randn(4, 16, device="cuda").bfloat16()
     dw = torch.empty(16, 64, device="cuda")
-    dp.dp_wgrad8(dw, dy, *g8)
+    dp.dp_wgrad8(dw, dy, *g8, ws=torch.empty(dp.dp_wgrad8_workspace_size(4, 16, 64), dtype=torch.uint8, device="cuda"))
     assert torch.isnan(dw[:, 32:]).all() and torch.isfinite(dw[:, :32]).all()
 
 
@@ -172,8 +172,8 @@ def test_weight_gradient(dev, rows, n, k, ldx, off, dtype, accumulate):
     dy = full[:, :n]
     old = torch.randn(n, k, generator=gen).to(dtype).cuda()
     dw, check = ou.flat_view(n * k, (n, k), dtype, off)
-    need = dp.dp_wgrad8_workspace_size(rows, n, k)
-    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") if need else None
+    need = dp.dp_wgrad8_workspace_size(rows, n, k, dy_aligned=ldx % 8 == 0)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     got = []
     for _ in range(2):
         dw.copy_(old)

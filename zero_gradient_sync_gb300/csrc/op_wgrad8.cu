@@ -1,31 +1,28 @@
 // Weight gradient from an 8-bit activation checkpoint:  dw[i][j] (+)= alpha sum_m dy[m][i] x[m][j],  x = code * step.
 //
 // A matrix product with the tokens m as its long axis: 2 m n k operations on m (2 n + k) bytes, so it belongs on the tensor
-// cores (tcgen05).  Decoding x to memory first would write and read 2 m k bytes more and hold a full bf16 copy; here the
-// codes are decoded on the way into shared memory, by warps that do nothing else.
+// cores (tcgen05).  The codes are first decoded into the workspace, once, as bf16 (exactly).  Decoding them on the way into
+// shared memory instead saves that pass (3 bytes a value, 15 us of 8k x 4096) but does it again for each 256 rows of dw:
+// measured with two teams of decoding warps beside the MMAs, the step of 64 tokens below took 0.47 us, 0.14 of it the
+// warps' shared-memory stores and 0.08 their arithmetic, against 0.27 us for operands that TMA brings.
 //
-// Two CTAs (a cluster) work on one 256 x 256 tile of dw with tcgen05.mma.cta_group::2: each holds 128 of the tile's rows
-// (dy columns) and decodes 128 of its columns; the pair shares both halves of x, so a step of 64 tokens costs each SM 16 KB of dy
-// and 16 KB of decoded x in shared memory against 512 cycles of matrix work.  One-CTA tiles would decode twice as much.
-// Both operands have the token as their row in memory, that is, the contraction is the slow axis ("MN-major" operands):
-// a slab of 64 columns x 64 tokens lies as 64 rows of 128 bytes, 128-byte swizzled, which is how TMA writes dy's slabs and
-// how the decoding warps write theirs.
+// Two CTAs (a cluster) work on one 256 x 256 tile of dw with tcgen05.mma.cta_group::2: each loads 128 of the tile's rows
+// (dy columns) and 128 of its columns (of x), and the pair shares both halves of x: 32 KB a step in each SM's shared memory
+// against 512 cycles of matrix work.  Both operands have the token as their row in memory, that is, the contraction is
+// the slow axis ("MN-major" operands): a slab of 64 columns x 64 tokens lies as 64 rows of 128 bytes, 128-byte swizzled,
+// as TMA writes it.
 //
-// Warps of a CTA: 0 loads dy by TMA; 1 (of the first CTA) issues the MMAs; 2 passes complete stages on; 4-11 take the
-// accumulators out of TMEM; 12-19 decode.  The decoders load their codes straight from global memory into registers, three
-// steps ahead: through shared memory they would take a quarter more of its bandwidth.
+// Warps of a CTA: 0 loads by TMA, both CTAs' copies counted by the first CTA's barrier; 1 (of the first CTA) issues the MMAs;
+// 4-11 take the accumulators out of TMEM.
 //
-// Sums: the tensor cores cut the sums that they accumulate in TMEM rather than round them, so the error of a long sum grows with
-// its length (5.7e-6 of the result's norm after 8192 tokens, where fp32 rounded at every step gives 5.4e-7).  So every
-// 512 tokens start a new accumulator, and the finished one is added, rounded, to sums that eight warps hold in registers
-// (128 a thread: setmaxnreg gives them what the other warps do without).  TMEM holds two accumulators, so the MMAs go on.
+// Sums: the tensor cores cut the sums that they accumulate in TMEM rather than round them, so the error of a long sum grows
+// with its length (5.7e-6 of the result's norm after 8192 tokens, where fp32 rounded at every step gives 5.4e-7).  So every
+// 512 tokens start a new accumulator, and the finished one is added, rounded, to sums that the eight warps hold in
+// registers, 128 a thread.  TMEM holds two accumulators, so the MMAs go on meanwhile.
 //
-// Decoding: with b = code bits, 0x4300 | (b & 0x7f) is the bf16 128 + (b & 0x7f), and 0x4300 | (b & 0x80) is 128, or 256 for a
-// negative code; their difference is the code, exactly, and times a power of two it stays exact: five instructions for two
-// values, no conversion instruction.
-//
-// Few tiles and many tokens: the tokens are split into slices, each slice's product goes to the workspace in fp32, and a
-// second kernel adds the slices in order.
+// Whole waves of tiles go to the CTA pairs as they are.  The tiles that are left over (all, where there are few) are
+// split over the tokens, as many slices as make the last waves shortest; a slice's product goes to the workspace in
+// fp32, and a second kernel adds the slices in order.
 //
 // Waits are bounded.  One that runs out makes the CTA stop and fill its tiles with NaN, which the step's check of the
 // gradients turns into a skipped step.
@@ -42,24 +39,18 @@ constexpr int SLAB = 64 * 128;                   // 64 tokens x 64 bf16
 constexpr int A_BYTES = 2 * SLAB, B_BYTES = 2 * SLAB, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGING = 32 * 33 * 4;             // a warp's 32 x 32 block of the result
 constexpr int CHUNK = 8;                         // steps of one accumulator
-constexpr int EPI0 = 4, EPI_WARPS = 8, DEC0 = 12, DEC_WARPS = 8;
-constexpr int THREADS = (DEC0 + DEC_WARPS) * 32;
-constexpr int AHEAD = 3;                         // steps of codes in registers; divides STAGES
-// Registers a thread: 96 at launch (640 threads); control warps give up 48, decoders 40, summing warps take 64: 48 + 2 * 160
-// + 2 * 56 = 5 * 96.
-constexpr int REGS_CONTROL = 48, REGS_SUM = 160, REGS_DECODE = 56;
-constexpr int BARS = 8 * (4 * STAGES + 7);
+constexpr int EPI0 = 4, EPI_WARPS = 8;
+constexpr int THREADS = (EPI0 + EPI_WARPS) * 32;  // 384: up to 168 registers each
+constexpr int BARS = 8 * (2 * STAGES + 7);
 constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * STAGING + 1024 + BARS;
-constexpr int MAX_SLICES = 32;
+constexpr int MAX_SLICES = 16;
 
 struct WgradParams {
-  const uint16_t* dy;
-  const int8_t* codes;
-  const uint8_t* scales;
   void* dw;
-  float* part;      // slices' products, or NULL for one slice
-  int64_t rows, n, k, lddy, pitch;
-  int64_t tiles_k, tiles, items, steps;  // steps: of 64 tokens, of one slice
+  float* part;      // [left-over tile][slice][256][256]
+  int64_t rows, n, k;
+  int32_t tiles_k, whole, left, slices;  // tiles of a row of tiles; tiles that are not split, that are; slices of these
+  int32_t items, all_steps, steps;       // steps of 64 tokens: all, of one slice
   float alpha;
   int dtype, accumulate;
   uint64_t timeout_ns;
@@ -92,18 +83,21 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
   if (mbar_try_wait(bar, parity)) return true;
   return wait_slow(bar, parity, timeout_ns, stop);
 }
-// Arrives at the barrier of the same shared-memory offset in CTA `rank` of the cluster.
-__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
-      : "memory");
+// The address of CTA `rank`'s barrier at the same shared-memory offset.
+__device__ __forceinline__ uint32_t bar_of(uint32_t bar, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(bar), "r"(rank));
+  return a;
 }
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_of(bar, rank)) : "memory");
+}
+// A tile into this CTA's shared memory, its bytes counted by a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t cluster_bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
 }
 // Shared-memory descriptor of an MN-major operand with 128-byte swizzle: slabs of 64 columns SLAB bytes apart (leading
@@ -137,110 +131,89 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
       : "r"(addr)
       : "memory");
 }
-// 32 bytes of codes, 32-byte aligned.
-__device__ __forceinline__ void load_codes(const int8_t* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
-}
-
-// Two bf16 values of two codes already spread over bytes 0 and 2: lo7 = 0x43 mm 0x43 mm, sign = 0x43 ss 0x43 ss.
-__device__ __forceinline__ uint32_t decode2(uint32_t lo7, uint32_t sign, __nv_bfloat162 step) {
-  const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&lo7);
-  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&sign);
-  const __nv_bfloat162 r = __hmul2(__hsub2(a, b), step);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint2 decode4(uint32_t w, __nv_bfloat162 step) {
-  const uint32_t lo = w & 0x7f7f7f7fu, hi = w & 0x80808080u;
-  return make_uint2(decode2(__byte_perm(lo, 0x43434343u, 0x4140), __byte_perm(hi, 0x43434343u, 0x4140), step),
-                    decode2(__byte_perm(lo, 0x43434343u, 0x4342), __byte_perm(hi, 0x43434343u, 0x4342), step));
-}
-
-// The tile, slice and first token of an item; items of one slice run through the tiles with dw's columns fastest, so
-// that CTAs that run together share dy's columns and the codes in L2.
+// An item: a tile, or a slice of one that is split.  Tiles run with dw's columns fastest, so that CTAs that run together
+// share dy's columns and x in L2.
 struct Item {
-  int64_t row0, col0, slice, token0;
-  int steps;
+  int32_t row0, col0, token0, steps;
+  int32_t part;  // of P.part, or -1
 };
-__device__ __forceinline__ Item item_at(const WgradParams& P, int64_t item) {
+__device__ __forceinline__ Item item_at(const WgradParams& P, int32_t item) {
   Item it;
-  it.slice = item / P.tiles;
-  const int64_t tile = item - it.slice * P.tiles;
-  const int64_t tr = tile / P.tiles_k;
+  int32_t tile = item, slice = 0;
+  it.part = -1;
+  it.token0 = 0;
+  it.steps = P.all_steps;
+  if (item >= P.whole) {
+    slice = (item - P.whole) / P.left;
+    const int32_t which = item - P.whole - slice * P.left;
+    tile = P.whole + which;
+    if (P.slices > 1) it.part = which * P.slices + slice;
+    it.token0 = slice * P.steps * BK;
+    const int32_t rest = P.all_steps - slice * P.steps;
+    it.steps = rest < P.steps ? rest : P.steps;
+  }
+  const int32_t tr = tile / P.tiles_k;
   it.row0 = tr * BM;
   it.col0 = (tile - tr * P.tiles_k) * BN;
-  it.token0 = it.slice * P.steps * BK;
-  const int64_t left = (P.rows - it.token0 + BK - 1) / BK;
-  it.steps = (int)(left < P.steps ? left : P.steps);
   return it;
-}
-
-// One element of the result of an item.
-__device__ __forceinline__ void put_result(const WgradParams& P, int64_t slice, int64_t row, int64_t col, float v) {
-  if (P.part) P.part[(slice * P.n + row) * P.k + col] = v;
-  else grad_put(P.dw, row * P.k + col, P.dtype, P.accumulate, v);
 }
 
 // Up to 32 rows of one column of a warp's block to memory.  Adding in fp32 is left to the L2: each element gets one
 // addition a call, so nothing depends on an order, and nobody waits for the old value.  bf16 has to be added in fp32 and
 // rounded once, so its old values are read, 8 rows in flight.
-__device__ __forceinline__ void store_block(const WgradParams& P, int64_t slice, int64_t row0, int64_t col, const float* block,
-                                            int rows) {
-  if (!P.part && P.dtype == DP_BF16) {
-    bf16_t* dst = static_cast<bf16_t*>(P.dw) + row0 * P.k + col;
-    for (int r0 = 0; r0 < rows; r0 += 8) {
+__device__ __forceinline__ void store_block(const WgradParams& P, int32_t part, int32_t row0, int32_t col0, int32_t r0,
+                                            int32_t c, const float* block, int rows) {
+  if (part < 0 && P.dtype == DP_BF16) {
+    bf16_t* dst = static_cast<bf16_t*>(P.dw) + (int64_t)(row0 + r0) * P.k + col0 + c;
+    for (int i = 0; i < rows; i += 8) {
       float old[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) old[r] = P.accumulate && r0 + r < rows ? bf16_to_f32(dst[r * P.k]) : 0.0f;
+      for (int r = 0; r < 8; ++r) old[r] = P.accumulate && i + r < rows ? bf16_to_f32(dst[r * P.k]) : 0.0f;
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (r0 + r < rows) dst[r * P.k] = bf16_rn(__fadd_rn(old[r], block[(r0 + r) * 33]));
+        if (i + r < rows) dst[r * P.k] = bf16_rn(__fadd_rn(old[r], block[(i + r) * 33]));
       dst += 8 * P.k;
     }
     return;
   }
-  float* dst = (P.part ? P.part + slice * P.n * P.k : static_cast<float*>(P.dw)) + row0 * P.k + col;
-  const bool add = !P.part && P.accumulate;
+  const int64_t ld = part >= 0 ? BN : P.k;
+  float* dst = part >= 0 ? P.part + ((int64_t)part * BM + r0) * BN + c
+                         : static_cast<float*>(P.dw) + (int64_t)(row0 + r0) * P.k + col0 + c;
+  const bool add = part < 0 && P.accumulate;
 #pragma unroll 4
   for (int r = 0; r < rows; ++r) {
     const float v = block[r * 33];
     if (add) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(dst), "f"(v) : "memory");
     else *dst = v;
-    dst += P.k;
+    dst += ld;
   }
 }
 
-template <bool TMA>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    wgrad8_kernel(const __grid_constant__ WgradParams P, const __grid_constant__ CUtensorMap map_dy) {
+    wgrad8_kernel(const __grid_constant__ WgradParams P, const __grid_constant__ CUtensorMap map_dy,
+                  const __grid_constant__ CUtensorMap map_x) {
   extern __shared__ char smem_raw[];
   const uint32_t smem0 = smem_u32(smem_raw);
   const uint32_t tiles = (smem0 + 1023) & ~1023u;  // the swizzle pattern repeats every 1024 bytes
-  char* smem = smem_raw + (tiles - smem0);
-  char* after = smem + STAGES * STAGE_BYTES;
+  char* after = smem_raw + (tiles - smem0) + STAGES * STAGE_BYTES;
   float* staging = reinterpret_cast<float*>(after);
   uint64_t* bars = reinterpret_cast<uint64_t*>(after + EPI_WARPS * STAGING);
   const uint32_t bar0 = smem_u32(bars);
-  auto a_full = [&](int s) { return bar0 + 8 * s; };
-  auto full = [&](int s) { return bar0 + 8 * (STAGES + s); };
-  auto empty = [&](int s) { return bar0 + 8 * (2 * STAGES + s); };
-  auto acc_full = [&](int b) { return bar0 + 8 * (3 * STAGES + b); };
-  auto acc_empty = [&](int b) { return bar0 + 8 * (3 * STAGES + 2 + b); };
-  auto decoded = [&](int s) { return bar0 + 8 * (3 * STAGES + 4 + s); };
-  const uint32_t drained = bar0 + 8 * (4 * STAGES + 4);
-  volatile int* stop = reinterpret_cast<int*>(bars + 4 * STAGES + 5);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 6);
+  auto full = [&](int s) { return bar0 + 8 * s; };  // (the first CTA's) both CTAs' halves of a stage are there
+  auto empty = [&](int s) { return bar0 + 8 * (STAGES + s); };
+  auto acc_full = [&](int b) { return bar0 + 8 * (2 * STAGES + b); };
+  auto acc_empty = [&](int b) { return bar0 + 8 * (2 * STAGES + 2 + b); };
+  const uint32_t drained = bar0 + 8 * (2 * STAGES + 4);
+  volatile int* stop = reinterpret_cast<int*>(bars + 2 * STAGES + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 6);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(a_full(s), 1);
-      mbar_init(decoded(s), DEC_WARPS);
-      mbar_init(full(s), 2);
+      mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -261,32 +234,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
-  if (warp < EPI0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONTROL));
   if (warp == 0) {
-    // ---------------------------------------------------------------- dy by TMA: two slabs of 64 columns a step
-    if (TMA && lane == 0) {
+    // ---------------------------------------------------------------- two slabs of dy and two of x a step
+    if (lane == 0) {
       int s = 0, phase = 0;
-      int64_t issued = 0;
       bool ok = true;
-      for (int64_t item = pair; ok && item < P.items; item += pairs) {
+      for (int32_t item = pair; ok && item < P.items; item += pairs) {
         const Item it = item_at(P, item);
-        const int x = (int)(it.row0 + rank * 128);
-        for (int i = 0; ok && i < it.steps; ++i) {
+        const int xa = it.row0 + (int)rank * 128, xb = it.col0 + (int)rank * 128;
+        for (int i = 0; i < it.steps; ++i) {
           ok = wait_bar(empty(s), phase ^ 1, P.timeout_ns, stop);
           if (!ok) break;
-          const uint32_t a = tiles + s * STAGE_BYTES;
-          const int y = (int)(it.token0 + (int64_t)i * BK);
-          mbar_arrive_expect_tx(a_full(s), A_BYTES);
-          tma_load(a, &map_dy, x, y, a_full(s));
-          tma_load(a + SLAB, &map_dy, x + 64, y, a_full(s));
-          ++issued;
+          const uint32_t a = tiles + s * STAGE_BYTES, bar = bar_of(full(s), 0);
+          const int y = it.token0 + i * BK;
+          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * STAGE_BYTES);
+          tma_load(a, &map_dy, xa, y, bar);
+          tma_load(a + SLAB, &map_dy, xa + 64, y, bar);
+          tma_load(a + A_BYTES, &map_x, xb, y, bar);
+          tma_load(a + A_BYTES + SLAB, &map_x, xb + 64, y, bar);
           if (++s == STAGES) s = 0, phase ^= 1;
         }
       }
-      if (!ok) {  // the copies still in flight land before the CTA may end
-        volatile int none = 0;
-        for (int64_t q = issued > STAGES ? issued - STAGES : 0; q < issued; ++q)
-          wait_bar(a_full((int)(q % STAGES)), (uint32_t)(q / STAGES) & 1, P.timeout_ns, &none);
+      if (!ok) {  // the copies in flight land before the CTA may end: a millisecond is far more than they take
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000) __nanosleep(1000);
       }
     }
   } else if (warp == 1) {
@@ -294,9 +265,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (rank == 0 && lane == 0) {
       int s = 0, phase = 0, b = 0, bphase = 0;
       bool ok = true;
-      for (int64_t item = pair; ok && item < P.items; item += pairs) {
-        const Item it = item_at(P, item);
-        for (int i = 0; i < it.steps; ++i) {
+      for (int32_t item = pair; ok && item < P.items; item += pairs) {
+        const int steps = item_at(P, item).steps;
+        for (int i = 0; i < steps; ++i) {
           const bool fresh = i % CHUNK == 0;
           ok = (!fresh || wait_bar(acc_empty(b), bphase ^ 1, P.timeout_ns, stop)) && wait_bar(full(s), phase, P.timeout_ns, stop);
           if (!ok) break;
@@ -307,7 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             mma_pair(tmem + b * BN, operand_desc(a + q * 2048), operand_desc(a + A_BYTES + q * 2048), !fresh || q != 0);
           commit_pair(empty(s));
           if (++s == STAGES) s = 0, phase ^= 1;
-          if (i % CHUNK == CHUNK - 1 || i == it.steps - 1) {
+          if (i % CHUNK == CHUNK - 1 || i == steps - 1) {
             commit_pair(acc_full(b));
             if (++b == 2) b = 0, bphase ^= 1;
           }
@@ -319,34 +290,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         wait_bar(drained, 0, P.timeout_ns, &none);
       }
     }
-  } else if (warp == 2) {
-    // ---------------------------------------------------------------- stages complete in this CTA -> the pair's MMAs
-    // This warp orders the decoders' writes before the tensor cores' reads and tells the first CTA.  The decoders do not
-    // do so themselves: the fence and the cluster-wide release would wait for the codes that they have in flight.
-    if (lane == 0) {
-      int s = 0, phase = 0;
-      bool ok = true;
-      for (int64_t item = pair; ok && item < P.items; item += pairs) {
-        const int steps = item_at(P, item).steps;
-        for (int i = 0; ok && i < steps; ++i) {
-          ok = (!TMA || wait_bar(a_full(s), phase, P.timeout_ns, stop)) && wait_bar(decoded(s), phase, P.timeout_ns, stop);
-          if (!ok) break;
-          fence_proxy_async_smem();
-          arrive_at(full(s), 0);
-          if (++s == STAGES) s = 0, phase ^= 1;
-        }
-      }
-    }
-  } else if (warp >= EPI0 && warp < DEC0) {
+  } else if (warp >= EPI0) {
     // ---------------------------------------------------------------- sums, and the result to memory
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SUM));
     const int quad = warp & 3;               // TMEM lanes 32 quad .. + 31: a warp may read no others
     const int half = (warp - EPI0) >> 2;     // columns 128 half .. + 127
     float* mine = staging + (warp - EPI0) * (32 * 33);
     const uint32_t from = tmem + ((uint32_t)quad << 21) + half * 128;
     int b = 0, bphase = 0;
     bool ok = true;
-    for (int64_t item = pair; ok && item < P.items; item += pairs) {
+    for (int32_t item = pair; ok && item < P.items; item += pairs) {
       float sum[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.0f;
@@ -369,8 +321,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       if (!ok) break;
       const Item it = item_at(P, item);
-      const int64_t row0 = it.row0 + rank * 128 + quad * 32;
-      const int rows = (int)(row0 >= P.n ? 0 : P.n - row0 < 32 ? P.n - row0 : 32);
+      const int r0 = (int)rank * 128 + quad * 32;
+      const int64_t there = P.n - it.row0 - r0;
+      const int rows = (int)(there < 0 ? 0 : there < 32 ? there : 32);
 #pragma unroll
       for (int c = 0; c < 128; c += 32) {
         __syncwarp();  // the previous block has been read
@@ -378,98 +331,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 32; ++i) mine[lane * 33 + i] = sum[c + i] * P.alpha;
         __syncwarp();
         // Row by row: 32 lanes, 32 consecutive columns.
-        const int64_t col = it.col0 + half * 128 + c + lane;
-        if (col < P.k) store_block(P, it.slice, row0, col, mine + lane, rows);
-      }
-    }
-  } else if (warp >= DEC0) {
-    // ---------------------------------------------------------------- codes to bf16 tiles
-    // A thread decodes one group of 32 codes of one token a step; a warp 8 tokens x 4 groups.  Eight neighbours, whose
-    // 16-byte stores go together, hold 4 tokens x 2 groups of one slab: the swizzle puts these into 8 different places.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DECODE));
-    const int t = threadIdx.x - DEC0 * 32;
-    const int token = (t >> 5) * 8 + ((t >> 4) & 1) * 4 + ((t >> 1) & 3), q = ((t >> 3) & 1) * 2 + (t & 1);
-    uint32_t c[AHEAD][8];
-    uint32_t E[AHEAD];
-    // The loading side runs AHEAD steps before the decoding side.  Where a token or a group is beyond the end, the step 0
-    // makes zeros of whatever codes the registers hold.
-    int64_t litem = pair;
-    int lsteps = 0, lvalid = 0;      // steps of the item, and of them this thread's, still to load
-    const int8_t* code_at = nullptr;
-    const uint8_t* scale_at = nullptr;
-    const int64_t code_step = BK * P.pitch, scale_step = BK * (P.pitch / DP_CKPT8_GROUP);
-    auto load = [&](uint32_t (&w)[8], uint32_t& e) {
-      if (lsteps == 0) {
-        if (litem >= P.items) return;
-        const Item it = item_at(P, litem);
-        litem += pairs;
-        lsteps = it.steps;
-        const int64_t m = it.token0 + token, col = it.col0 + rank * 128 + q * 32;
-        const int64_t valid = col < P.pitch && m < P.rows ? (P.rows - m + BK - 1) / BK : 0;
-        lvalid = (int)(valid < lsteps ? valid : lsteps);
-        code_at = P.codes + m * P.pitch + col;
-        scale_at = P.scales + m * (P.pitch / DP_CKPT8_GROUP) + col / DP_CKPT8_GROUP;
-      }
-      e = 0;
-      if (lvalid > 0) {
-        load_codes(code_at, w);
-        e = __ldg(scale_at);
-      }
-      code_at += code_step;
-      scale_at += scale_step;
-      --lvalid;
-      --lsteps;
-    };
-    int64_t total = 0;
-    for (int64_t item = pair; item < P.items; item += pairs) total += item_at(P, item).steps;
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[u][i] = 0;
-      E[u] = 0;
-      load(c[u], E[u]);
-    }
-    // The thread's four 16-byte pieces: slab q / 2, row `token`, piece p at place p ^ (token mod 8).
-    char* line = smem + A_BYTES + (q >> 1) * SLAB + token * 128;
-    const uint32_t first = ((uint32_t)(q & 1) * 4 ^ (uint32_t)(token & 7)) << 4;
-    int64_t citem = pair;            // (without TMA) the item and step whose dy is copied
-    int ci = 0;
-    uint32_t phase = 1;
-    bool ok = true;
-    for (int64_t done = 0; ok && done < total; done += STAGES, phase ^= 1) {
-#pragma unroll
-      for (int s = 0; s < STAGES; ++s) {
-        if (done + s >= total) break;
-        const int u = s % AHEAD;
-        // A step byte is a bf16's exponent.  255, an infinity, makes NaNs of the zero codes of such a group.
-        const uint32_t sb = __byte_perm(E[u] << 7, 0, 0x1010);
-        const __nv_bfloat162 step = *reinterpret_cast<const __nv_bfloat162*>(&sb);
-        ok = wait_bar(empty(s), phase, P.timeout_ns, stop);
-        if (!ok) break;
-        char* to = line + s * STAGE_BYTES;
-#pragma unroll
-        for (uint32_t p = 0; p < 4; ++p) {
-          const uint2 lo = decode4(c[u][2 * p], step), hi = decode4(c[u][2 * p + 1], step);
-          *reinterpret_cast<uint4*>(to + (first ^ (p << 4))) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        }
-        load(c[u], E[u]);
-        if (!TMA) {
-          // dy's rows are not 16-byte aligned: the decoders copy its tile too, one element at a time.
-          const Item it = item_at(P, citem);
-          const int64_t m0 = it.token0 + (int64_t)ci * BK, n0 = it.row0 + rank * 128;
-          char* stage = smem + s * STAGE_BYTES;
-#pragma unroll 4
-          for (int e = t; e < BK * 128; e += DEC_WARPS * 32) {
-            const int tok = e >> 7, col = e & 127;
-            uint16_t v = 0;
-            if (m0 + tok < P.rows && n0 + col < P.n) v = P.dy[(m0 + tok) * P.lddy + n0 + col];
-            *reinterpret_cast<uint16_t*>(stage + (col >> 6) * SLAB + tok * 128 + ((((col & 63) >> 3) ^ (tok & 7)) << 4) +
-                                         (col & 7) * 2) = v;
-          }
-          if (++ci == it.steps) ci = 0, citem += pairs;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(decoded(s));
+        const int col = half * 128 + c + lane;
+        if (it.col0 + col < P.k) store_block(P, it.part, it.row0, it.col0, r0, col, mine + lane, rows);
       }
     }
   }
@@ -481,53 +344,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   if (*stop) {
-    for (int64_t item = pair; item < P.items; item += pairs) {
+    for (int32_t item = pair; item < P.items; item += pairs) {
       const Item it = item_at(P, item);
+      const float nan = __uint_as_float(0x7fc00000u);
       for (int e = threadIdx.x; e < 128 * BN; e += THREADS) {
-        const int64_t row = it.row0 + rank * 128 + e / BN, col = it.col0 + e % BN;
-        if (row < P.n && col < P.k) put_result(P, it.slice, row, col, __uint_as_float(0x7fc00000u));
+        const int r = (int)rank * 128 + e / BN, c = e % BN;
+        if (it.row0 + r >= P.n || it.col0 + c >= P.k) continue;
+        if (it.part >= 0) P.part[((int64_t)it.part * BM + r) * BN + c] = nan;
+        else grad_put(P.dw, (int64_t)(it.row0 + r) * P.k + it.col0 + c, P.dtype, 0, nan);
       }
     }
   }
 }
 
-// dw (+)= the slices' products in order.
-__global__ void __launch_bounds__(256) wgrad8_join_kernel(const float* part, void* dw, int64_t size, int slices, int dtype,
-                                                          int accumulate) {
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < size; i += step) {
-    float v = 0.0f;
+// dw (+)= the slices' products in order, for the tiles that were split: one row of one tile a CTA.
+__global__ void __launch_bounds__(BN) wgrad8_join_kernel(const __grid_constant__ WgradParams P) {
+  const int which = blockIdx.x / BM, r = blockIdx.x % BM;
+  const int tile = P.whole + which, tr = tile / P.tiles_k;
+  const int64_t row = (int64_t)tr * BM + r, col = (int64_t)(tile - tr * P.tiles_k) * BN + threadIdx.x;
+  if (row >= P.n || col >= P.k) return;
+  const float* part = P.part + ((int64_t)which * P.slices * BM + r) * BN + threadIdx.x;
+  float v = 0.0f;
 #pragma unroll 4
-    for (int s = 0; s < slices; ++s) v += part[s * size + i];
-    grad_put(dw, i, dtype, accumulate, v);
-  }
+  for (int s = 0; s < P.slices; ++s) v += part[(int64_t)s * BM * BN];
+  grad_put(P.dw, row * P.k + col, P.dtype, P.accumulate, v);
+}
+
+// dy with rows that TMA cannot read, to rows of ld elements (a multiple of 8).
+__global__ void __launch_bounds__(256) wgrad8_copy_kernel(uint16_t* dst, int64_t ld, const uint16_t* src, int64_t lds, int64_t n) {
+  for (int64_t c = threadIdx.x; c < n; c += blockDim.x) dst[blockIdx.x * ld + c] = src[blockIdx.x * lds + c];
 }
 
 // ---------------------------------------------------------------------------------------------------- host side
 
 struct Split {
-  int64_t tiles_k, tiles, slices, steps;
+  int64_t tiles_k, tiles, whole, left, slices, all_steps, steps;
 };
-// Slices of the tokens: enough items for all CTA pairs, at least 4 steps (256 tokens) each, so that a slice's fp32 product
-// costs less than what it saves.
+// Whole waves of tiles stay whole.  The rest is split into the number of slices that takes the least time, counted in steps:
+// waves x (steps of a slice + 4 for storing its product).
 Split split_of(int64_t rows, int64_t n, int64_t k) {
   Split s;
+  const int64_t pairs = sm_count() / 2;
   s.tiles_k = (k + BN - 1) / BN;
   s.tiles = (n + BM - 1) / BM * s.tiles_k;
-  const int64_t all = (rows + BK - 1) / BK, pairs = 76;
-  s.slices = pairs / s.tiles;
-  if (s.slices > all / 4) s.slices = all / 4;
-  if (s.slices > MAX_SLICES) s.slices = MAX_SLICES;
-  if (s.slices < 1) s.slices = 1;
-  s.steps = all ? (all + s.slices - 1) / s.slices : 0;
-  if (all) s.slices = (all + s.steps - 1) / s.steps;
+  s.all_steps = (rows + BK - 1) / BK;
+  s.whole = s.tiles / pairs * pairs;
+  s.left = s.tiles - s.whole;
+  s.slices = 1;
+  int64_t best = s.all_steps + 4;
+  for (int64_t c = 2; s.left > 0 && c <= MAX_SLICES && c * 4 <= s.all_steps; ++c) {
+    const int64_t cost = (s.left * c + pairs - 1) / pairs * ((s.all_steps + c - 1) / c + 4);
+    if (cost < best) best = cost, s.slices = c;
+  }
+  s.steps = (s.all_steps + s.slices - 1) / s.slices;
+  if (s.all_steps) s.slices = (s.all_steps + s.steps - 1) / s.steps;
   return s;
+}
+struct WgradWs {
+  size_t part, dy, bytes;  // x lies at 0
+  int64_t lddy;
+};
+WgradWs ws_of(int64_t rows, int64_t n, int64_t k, const Split& s, bool aligned) {
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  WgradWs w;
+  w.part = up((size_t)rows * dp_ckpt8_pitch(k) * 2);
+  w.dy = w.part + (s.slices > 1 ? (size_t)s.left * s.slices * BM * BN * 4 : 0);
+  w.lddy = (n + 7) / 8 * 8;
+  w.bytes = w.dy + (aligned && n % 8 == 0 ? 0 : up((size_t)rows * w.lddy * 2));
+  return w;
 }
 
 dp_status_t check_product(int64_t rows, int64_t n, int64_t k) {
   if (rows < 0 || rows > INT32_MAX - BK) return op_fail(DP_ERR_INVALID_ARG, "rows = %lld not in 0..2^31-65", (long long)rows);
   if (n < 1 || n > (1 << 28)) return op_fail(DP_ERR_INVALID_ARG, "n = %lld not in 1..2^28", (long long)n);
   if (k < 1 || k > (1 << 28)) return op_fail(DP_ERR_INVALID_ARG, "k = %lld not in 1..2^28", (long long)k);
+  if (((n + BM - 1) / BM) * ((k + BN - 1) / BN) > (1 << 22)) return op_fail(DP_ERR_INVALID_ARG, "n x k = %lld x %lld is too large", (long long)n, (long long)k);
   return DP_OK;
 }
 
@@ -546,6 +437,18 @@ EncodeTiled encode_tiled() {
   return f;
 }
 
+// Rows of `cols` bf16 in boxes of 64 columns x 64 rows.
+dp_status_t map_of(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return op_fail(DP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, BK}, one[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DP_OK : op_fail(DP_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+}
+
 }  // namespace
 }  // namespace dp
 
@@ -553,10 +456,9 @@ using namespace dp;
 
 extern "C" {
 
-size_t dp_wgrad8_workspace_size(int64_t rows, int64_t n, int64_t k) {
+size_t dp_wgrad8_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dy_aligned) {
   if (check_product(rows, n, k) != DP_OK) return 0;
-  const Split s = split_of(rows, n, k);
-  return s.slices > 1 ? (size_t)s.slices * (size_t)n * (size_t)k * 4 : 0;
+  return ws_of(rows, n, k, split_of(rows, n, k), dy_aligned != 0).bytes;
 }
 
 dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t n,
@@ -571,8 +473,7 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
   DP_TRY(check_dev(dy, 2, rows > 0, "dy"));
   if (rows > 0 && (!codes || !scales)) return op_fail(DP_ERR_INVALID_ARG, "codes or scales are NULL");
   if (!is_aligned(codes, 32)) return op_fail(DP_ERR_ALIGNMENT, "codes are not 32-byte aligned");
-  const Split s = split_of(rows, n, k);
-  DP_TRY(check_dev(ws, 256, s.slices > 1, "ws"));
+  DP_TRY(check_dev(ws, 256, rows > 0, "ws"));
   const cudaStream_t stream = (cudaStream_t)stream_;
   NvtxRange range("weight gradient");
   if (rows == 0) {
@@ -580,48 +481,47 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
     const cudaError_t e = cudaMemsetAsync(dw, 0, (size_t)(n * k) * elem_size(dtype), stream);
     return e == cudaSuccess ? DP_OK : op_fail(DP_ERR_CUDA, "weight gradient fill: %s", cudaGetErrorString(e));
   }
+  // TMA wants 16-byte aligned rows; other rows are copied to aligned ones first (a twentieth of the product's time at most).
+  const bool aligned = is_aligned(dy, 16) && lddy % 8 == 0;
+  const Split s = split_of(rows, n, k);
+  const WgradWs w = ws_of(rows, n, k, s, aligned);
+  char* base = static_cast<char*>(ws);
+  const int64_t pitch = dp_ckpt8_pitch(k);
+  CUtensorMap map_x, map_dy;
+  DP_TRY(map_of(&map_x, base, pitch, rows, pitch));
+  DP_TRY(map_of(&map_dy, aligned ? (const void*)dy : base + w.dy, n, rows, aligned ? lddy : w.lddy));
+  const cudaError_t attr = cudaFuncSetAttribute(wgrad8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (attr != cudaSuccess) return op_fail(DP_ERR_CUDA, "weight gradient: %s", cudaGetErrorString(attr));
+  DP_TRY(dp_ckpt8_decode(base, codes, scales, rows, pitch, pitch, DP_BF16, stream_));
+  int launches = 1;
+  if (!aligned) {
+    wgrad8_copy_kernel<<<(unsigned)rows, 256, 0, stream>>>(reinterpret_cast<uint16_t*>(base + w.dy), w.lddy, dy, lddy, n);
+    ++launches;
+  }
   WgradParams P = {};
-  P.dy = dy;
-  P.codes = codes;
-  P.scales = scales;
   P.dw = dw;
-  P.part = s.slices > 1 ? static_cast<float*>(ws) : nullptr;
+  P.part = reinterpret_cast<float*>(base + w.part);
   P.rows = rows;
   P.n = n;
   P.k = k;
-  P.lddy = lddy;
-  P.pitch = dp_ckpt8_pitch(k);
-  P.tiles_k = s.tiles_k;
-  P.tiles = s.tiles;
-  P.items = s.tiles * s.slices;
-  P.steps = s.steps;
+  P.tiles_k = (int32_t)s.tiles_k;
+  P.whole = (int32_t)s.whole;
+  P.left = (int32_t)s.left;
+  P.slices = (int32_t)s.slices;
+  P.items = (int32_t)(s.whole + s.left * s.slices);
+  P.all_steps = (int32_t)s.all_steps;
+  P.steps = (int32_t)s.steps;
   P.alpha = alpha;
   P.dtype = dtype;
   P.accumulate = accumulate;
   P.timeout_ns = dp_get_wait_timeout_ns();
-  // TMA wants 16-byte aligned rows; other rows are copied by the decoding warps.
-  const bool tma = is_aligned(dy, 16) && lddy % 8 == 0;
-  CUtensorMap map = {};
-  if (tma) {
-    const EncodeTiled encode = encode_tiled();
-    if (!encode) return op_fail(DP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dims[2] = {(cuuint64_t)n, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)lddy * 2};
-    const cuuint32_t box[2] = {64, BK}, one[2] = {1, 1};
-    const CUresult r = encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(dy), dims, strides, box, one,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return op_fail(DP_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
-  }
-  auto kernel = tma ? wgrad8_kernel<true> : wgrad8_kernel<false>;
-  const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (attr != cudaSuccess) return op_fail(DP_ERR_CUDA, "weight gradient: %s", cudaGetErrorString(attr));
   const int64_t pairs = sm_count() / 2;
-  kernel<<<(unsigned)(2 * (P.items < pairs ? P.items : pairs)), THREADS, SMEM, stream>>>(P, map);
-  if (!P.part) return op_launched("weight gradient launch", 1);
-  const int64_t size = n * k, ctas = (size + 1023) / 1024, most = (int64_t)sm_count() * 8;
-  wgrad8_join_kernel<<<(unsigned)(ctas < most ? ctas : most), 256, 0, stream>>>(P.part, dw, size, (int)s.slices, dtype,
-                                                                               accumulate);
-  return op_launched("weight gradient launch", 2);
+  wgrad8_kernel<<<(unsigned)(2 * (P.items < pairs ? P.items : pairs)), THREADS, SMEM, stream>>>(P, map_dy, map_x);
+  if (s.slices > 1) {
+    wgrad8_join_kernel<<<(unsigned)(s.left * BM), BN, 0, stream>>>(P);
+    ++launches;
+  }
+  return op_launched("weight gradient launch", launches);
 }
 
 }  // extern "C"

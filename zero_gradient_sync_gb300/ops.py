@@ -42,7 +42,7 @@ def _declare() -> None:
         "dp_ckpt8_decode": (c_i32, [c_vp] * 3 + [c_i64] * 3 + [c_i32, c_vp]),
         "dp_act_ckpt8": (c_i32, [c_vp] * 7 + [c_i64] * 4 + [c_i32, c_vp]),
         "dp_act_ckpt8_grad": (c_i32, [c_vp] * 8 + [c_i64] * 4 + [c_i32, c_vp]),
-        "dp_wgrad8_workspace_size": (size_t, [c_i64] * 3),
+        "dp_wgrad8_workspace_size": (size_t, [c_i64] * 3 + [c_i32]),
         "dp_wgrad8": (c_i32, [c_vp] * 4 + [c_i64] * 4 + [c_f32, c_i32, c_i32, c_vp, c_vp]),
     }
     for name, (res, args) in sig.items():
@@ -286,16 +286,18 @@ def dp_act_ckpt8_grad(dg, du, dh, *, act: int = DP_ACT_SILU, g8=None, u8=None, h
                                  act, _stream(stream)), "dp_act_ckpt8_grad")
 
 
-def dp_wgrad8_workspace_size(rows: int, n: int, k: int) -> int:
-    """Bytes of workspace of dp_wgrad8 (0: none is needed)."""
-    return int(LIB.dp_wgrad8_workspace_size(rows, n, k))
+def dp_wgrad8_workspace_size(rows: int, n: int, k: int, dy_aligned: bool = True) -> int:
+    """Bytes of workspace of dp_wgrad8.  dy_aligned: dy's rows are 16-byte aligned where n is a multiple of 8 (a contiguous dy's
+    are)."""
+    return int(LIB.dp_wgrad8_workspace_size(rows, n, k, 1 if dy_aligned else 0))
 
 
 def dp_wgrad8(dw, dy, codes, scales, alpha: float = 1.0, accumulate: bool = False, ws=None, stream=None) -> None:
-    """dw [n, k] (+)= alpha * dy^T x for dy [rows, n] (bfloat16) and the 8-bit checkpoint of x [rows, k]."""
+    """dw [n, k] (+)= alpha * dy^T x for dy [rows, n] (bfloat16) and the 8-bit checkpoint of x [rows, k].  ws:
+    dp_wgrad8_workspace_size bytes."""
     (n, k), (rows, n2) = _matrix(dw, "dw"), _matrix(dy, "dy")
     py, ld = _rows(dy, (rows, n), _BF16, "dy")
     pc, ps = _ckpt(codes, scales, rows, k, "checkpoint")
-    need = LIB.dp_wgrad8_workspace_size(rows, n, k)
+    need = LIB.dp_wgrad8_workspace_size(rows, n, k, 1 if py % 16 == 0 and ld % 8 == 0 else 0) if rows else 0
     _check(LIB.dp_wgrad8(_arg(dw, (n, k), dw.dtype, "dw"), py, pc, ps, rows, n, k, ld, alpha, 1 if accumulate else 0,
                          _dtype(dw, "dw"), _ws(ws, need), _stream(stream)), "dp_wgrad8")
