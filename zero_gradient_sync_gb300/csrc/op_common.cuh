@@ -29,6 +29,24 @@ struct Elem<float> {
   static __device__ __forceinline__ float put(float v) { return v; }
 };
 
+// Packed pairs of fp32 beside dp_device.cuh's.
+__device__ __forceinline__ f2_t f2_fma(f2_t a, f2_t b, f2_t c) {
+  f2_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2_t f2_both(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ float f2_sum(f2_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ uint32_t f2_to_bf16x2(f2_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return bf16x2_rn(a, b);
+}
+
 // Eight elements as they lie in memory: one 16-byte word of bf16, two of fp32.
 template <typename T>
 struct Raw8;
@@ -38,6 +56,12 @@ struct Raw8<bf16_t> {
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
     v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+  }
+  __device__ __forceinline__ void unpack2(f2_t (&v)[4]) const {
+    v[0] = bf16x2_to_f2(a.x); v[1] = bf16x2_to_f2(a.y); v[2] = bf16x2_to_f2(a.z); v[3] = bf16x2_to_f2(a.w);
+  }
+  __device__ __forceinline__ void pack2(const f2_t (&v)[4]) {
+    a = make_uint4(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]), f2_to_bf16x2(v[2]), f2_to_bf16x2(v[3]));
   }
   __device__ __forceinline__ void pack(const float (&v)[8]) {
     a.x = bf16x2_rn(v[0], v[1]); a.y = bf16x2_rn(v[2], v[3]);
@@ -49,6 +73,15 @@ struct Raw8<float> {
   float4 a, b;
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ __forceinline__ void unpack2(f2_t (&v)[4]) const {
+    v[0] = f2_pack(a.x, a.y); v[1] = f2_pack(a.z, a.w); v[2] = f2_pack(b.x, b.y); v[3] = f2_pack(b.z, b.w);
+  }
+  __device__ __forceinline__ void pack2(const f2_t (&v)[4]) {
+    f2_unpack(v[0], a.x, a.y);
+    f2_unpack(v[1], a.z, a.w);
+    f2_unpack(v[2], b.x, b.y);
+    f2_unpack(v[3], b.z, b.w);
   }
   __device__ __forceinline__ void pack(const float (&v)[8]) {
     a = make_float4(v[0], v[1], v[2], v[3]);
@@ -71,9 +104,16 @@ __device__ __forceinline__ Raw8<float> load_raw8(const float* p) {
 __device__ __forceinline__ void store_raw8(bf16_t* p, const Raw8<bf16_t>& r) {
   *reinterpret_cast<uint4*>(p) = r.a;
 }
+// Eight fp32 as one 32-byte store where the address allows it: two 16-byte stores touch every sector twice.
 __device__ __forceinline__ void store_raw8(float* p, const Raw8<float>& r) {
-  reinterpret_cast<float4*>(p)[0] = r.a;
-  reinterpret_cast<float4*>(p)[1] = r.b;
+  if (((uintptr_t)p & 31) == 0) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(r.a.x), "f"(r.a.y), "f"(r.a.z),
+                 "f"(r.a.w), "f"(r.b.x), "f"(r.b.y), "f"(r.b.z), "f"(r.b.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<float4*>(p)[0] = r.a;
+    reinterpret_cast<float4*>(p)[1] = r.b;
+  }
 }
 
 // A parameter of either type, at any element offset; NULL stands for `none`.
@@ -93,7 +133,26 @@ __device__ __forceinline__ void grad_put(void* p, int64_t i, int dtype, int accu
   }
 }
 
+// Kernels of one call may be launched so that each is set up before the one ahead of it has ended: grid_wait waits for that end
+// (and its writes), grid_go lets the next one be set up.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- host side
+
+template <typename K, typename P>
+cudaError_t launch_after(K kernel, int64_t ctas, dim3 threads, cudaStream_t stream, const P& params) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)ctas);
+  c.blockDim = threads;
+  c.stream = stream;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, params);
+}
 
 inline dp_status_t op_fail(dp_status_t s, const char* fmt, ...) {
   char msg[256];

@@ -57,10 +57,6 @@ inline EmbWs emb_ws(int64_t tokens, int64_t dim) {
   return w;
 }
 
-// The gradient's kernels are launched so that each may be set up before the one ahead of it has ended; this waits for that end.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ------------------------------------------------------------------------------------------------------- lookup
 
 template <typename T>
@@ -588,28 +584,15 @@ cudaError_t launch_sort(const SortParams& S, cudaStream_t stream) {
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, emb_sort_kernel<CTAS>, S);
 }
-template <typename K>
-cudaError_t launch_after(K kernel, int64_t ctas, int threads, cudaStream_t stream, const SumParams& P) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)ctas);
-  c.blockDim = dim3(threads);
-  c.stream = stream;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = a;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, P);
-}
 template <typename T, int VEC>
 cudaError_t launch_sum(const SumParams& P, cudaStream_t stream) {
   const int64_t chunks = (P.tokens + P.chunk - 1) / P.chunk;
   const int64_t ctas = (chunks * P.slabs + 3) / 4;
-  const cudaError_t e = P.accumulate ? launch_after(emb_sum_kernel<T, VEC, true>, ctas, 128, stream, P)
-                                     : launch_after(emb_sum_kernel<T, VEC, false>, ctas, 128, stream, P);
+  const cudaError_t e = P.accumulate ? launch_after(emb_sum_kernel<T, VEC, true>, ctas, dim3(128), stream, P)
+                                     : launch_after(emb_sum_kernel<T, VEC, false>, ctas, dim3(128), stream, P);
   if (e != cudaSuccess) return e;
   const int64_t runs = (chunks + JOIN_WARPS - 1) / JOIN_WARPS, most = (sm_count() * 16 + P.slabs - 1) / P.slabs;
-  return launch_after(emb_join_kernel<T, VEC>, (runs < most ? runs : most) * P.slabs, JOIN_WARPS * 32, stream, P);
+  return launch_after(emb_join_kernel<T, VEC>, (runs < most ? runs : most) * P.slabs, dim3(JOIN_WARPS * 32), stream, P);
 }
 
 }  // namespace

@@ -8,8 +8,8 @@
 //
 // A row is held by a group of threads, eight consecutive elements each (or one element every group-width where rows are
 // not 16-byte aligned), NV such pieces a thread.  A group is one warp for short rows, else the whole CTA; CTAs are
-// persistent, so parameters are read once per CTA and held in registers, and the next row's loads are issued before the
-// current row's sums.  Mean and variance are taken in two passes over the registers: no cancellation.
+// persistent, so parameters are read once per CTA and held in registers, and the next rows are on their way to shared memory
+// while a row is summed (three rows ahead at 4096 columns: 96 KB in flight an SM).  Mean and variance are taken in two passes over the registers: no cancellation.
 //
 // Gradient, with yh, rh the rows before weights and biases, D = dr + N_pre'(dz) and q = g D for a gate per token, else D:
 //   v  = w_pre dz:      D  = dr + rstd_pre (v - rh mean(v rh) - mean(v))          (RMS: without mean(v))
@@ -30,7 +30,8 @@ namespace {
 
 constexpr int NORM_THREADS = 512;   // most threads of a group
 constexpr int MAX_PARTS = 1024;     // most CTAs (partial rows) of the gradient
-constexpr int FIN_COLS = 32, FIN_ROWS = 16;
+constexpr int FIN_COLS = 16, FIN_ROWS = 64;
+constexpr int MAX_SLOTS = 4;
 
 struct NormParams {
   void *r, *z, *dx, *dy, *dgate_token;
@@ -39,8 +40,8 @@ struct NormParams {
   float2 *post_stats, *pre_stats;
   float* part;
   int64_t rows;
-  int dim, group, per_cta;  // threads of a row, rows of a CTA at a time
-  int layer, post, pre, gate_mode, pdt, accumulate;
+  int dim, group, per_cta, slots;  // threads of a row, rows of a CTA at a time, rows in flight
+  int layer, post, pre, gate_mode, pdt, accumulate, bias;
   float eps, a, b;
 };
 
@@ -50,31 +51,60 @@ __device__ __forceinline__ int col_of(int tid, int group, int j, int k) {
   return VEC ? (tid + j * group) * 8 + k : tid + (j * 8 + k) * group;
 }
 
+// A row's pieces in a thread's registers.  Rows whose pieces are 16-byte words pass through shared memory, P.slots - 1 rows
+// ahead.  A slot is an image of the row, and a warp copies just the part that its own threads read: no barrier wider than
+// the warp is needed.
 template <typename T, int VEC, int NV>
 struct RowRegs {
+  static constexpr int WORDS = sizeof(T) / 2;  // 16-byte words of eight elements
   Raw8<T> w[NV];
-  __device__ __forceinline__ void load(const T* row, int tid, int group, int dim) {
+  static __device__ __forceinline__ int bytes(int group) { return NV * group * 16 * WORDS; }
+  static __device__ __forceinline__ void fetch(char* slot, const T* row, int tid, int group, int dim) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int q = 0; q < WORDS; ++q) {  // neighbours copy neighbouring words
+        const int at = (j * group + (tid & ~31)) * 16 * WORDS + q * 512 + (tid & 31) * 16;
+        if (at < dim * (int)sizeof(T))
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot + at)),
+                       "l"(reinterpret_cast<const char*>(row) + at)
+                       : "memory");
+      }
+    }
+  }
+  // From the slot, or (not VEC) from the row itself; pieces beyond dim are zeros.
+  __device__ __forceinline__ void load(const char* slot, const T* row, int tid, int group, int dim) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       if (VEC) {
-        const int c = col_of<1>(tid, group, j, 0);
-        if (c < dim) w[j] = load_raw8(row + c);
-        else {
-          const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          w[j].pack(zero);
+        if (col_of<1>(tid, group, j, 0) < dim) {
+          uint4* to = reinterpret_cast<uint4*>(&w[j]);
+#pragma unroll
+          for (int q = 0; q < WORDS; ++q) to[q] = *reinterpret_cast<const uint4*>(slot + ((j * group + tid) * WORDS + q) * 16);
+        } else {
+          w[j].pack(v);
         }
       } else {
-        float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int c = col_of<0>(tid, group, j, k);
-          v[k] = c < dim ? Elem<T>::get(row[c]) : 0.0f;
+          if (c < dim) v[k] = Elem<T>::get(row[c]);
         }
         w[j].pack(v);
       }
     }
   }
 };
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but the last `rows` fetched rows are there.
+__device__ __forceinline__ void fetch_wait(int rows) {
+  if (rows == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (rows == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (rows == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+}
 
 template <typename T, int VEC, int NV>
 __device__ __forceinline__ void store_row(T* row, int tid, int group, int dim, const float (&v)[NV][8]) {
@@ -97,6 +127,29 @@ __device__ __forceinline__ void store_row(T* row, int tid, int group, int dim, c
   }
 }
 
+// The same from pairs of elements.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void store_row2(T* row, int tid, int group, int dim, const f2_t (&v)[NV][4]) {
+  if (VEC) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = col_of<1>(tid, group, j, 0);
+      if (c < dim) {
+        Raw8<T> o;
+        o.pack2(v[j]);
+        store_raw8(row + c, o);
+      }
+    }
+  } else {
+    float x[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f2_unpack(v[j][k], x[j][2 * k], x[j][2 * k + 1]);
+    store_row<T, 0, NV>(row, tid, group, dim, x);
+  }
+}
+
 template <int VEC, int NV>
 __device__ __forceinline__ void load_param(const void* p, int dtype, float none, int tid, int group, int dim,
                                            float (&v)[NV][8]) {
@@ -110,33 +163,39 @@ __device__ __forceinline__ void load_param(const void* p, int dtype, float none,
 }
 
 // Sums of N values over a group of threads; every thread gets them.  A CTA-wide group alternates between two halves of
-// `buf`, so one barrier a call is enough: a half is written again only after the barrier of the call in between.
+// `buf` (zero beyond the group's warps), so one barrier a call is enough: a half is written again only after the barrier
+// of the call in between.  The warps' sums are read as broadcast words, which takes less than another five shuffles.
+typedef float GroupBuf[2][3][16];
 template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], int warps, float (*buf)[32][4], int& half) {
+__device__ __forceinline__ void group_sum(float (&v)[N], int warps, GroupBuf& buf, int& half) {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if (warps == 1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) buf[half][warp][i] = v[i];
+    for (int i = 0; i < N; ++i) buf[half][i][warp] = v[i];
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    v[i] = lane < warps ? buf[half][lane][i] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    const float4* p = reinterpret_cast<const float4*>(buf[half][i]);
+    const float4 a = p[0], b = p[1], c = p[2], d = p[3];
+    v[i] = (((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w))) + (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
   }
   half ^= 1;
+}
+__device__ __forceinline__ void clear(GroupBuf& buf) {
+  for (int i = threadIdx.x; i < 96; i += blockDim.x) (&buf[0][0][0])[i] = 0.0f;
+  __syncthreads();
 }
 
 // Mean (0 for RMS) and 1 / sqrt(var + eps) of a row held in registers.  Pieces beyond dim hold zeros.
 template <int VEC, int NV>
 __device__ __forceinline__ float2 row_stats(const float (&v)[NV][8], int layer, float eps, int tid, int group, int dim,
-                                            float (*buf)[32][4], int& half) {
+                                            GroupBuf& buf, int& half) {
   float mean = 0.0f, s[1];
   if (layer) {
     s[0] = 0.0f;
@@ -171,10 +230,27 @@ __device__ __forceinline__ int64_t first_row(const NormParams& P, int& tid) {
 
 template <typename TS, typename TB, int VEC, int NV>
 __global__ void __launch_bounds__(NORM_THREADS) norm_kernel(const __grid_constant__ NormParams P) {
-  __shared__ float buf[2][32][4];
+  extern __shared__ char slots[];
+  __shared__ __align__(16) GroupBuf buf;
+  clear(buf);
+  typedef RowRegs<TS, VEC, NV> RowS;
+  typedef RowRegs<TB, VEC, NV> RowB;
   int half = 0, tid;
   const int64_t row0 = first_row(P, tid), step = (int64_t)gridDim.x * P.per_cta;
   const int group = P.group, dim = P.dim;
+  const int at_x = RowB::bytes(group), slot_bytes = at_x + RowS::bytes(group);
+  char* mine = slots + (P.per_cta == 1 ? 0 : (threadIdx.x >> 5) * P.slots * slot_bytes);
+  auto fetch = [&](int64_t row, int slot) {
+    if (VEC) __syncwarp();  // the slot's last row has been read
+    if (VEC && row < P.rows) {
+      char* to = mine + slot * slot_bytes;
+      if (P.y) RowB::fetch(to, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+      RowS::fetch(to + at_x, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
+    }
+    if (VEC) fetched();
+  };
+  for (int s = 0; s + 1 < P.slots; ++s) fetch(row0 + s * step, s);
+  int slot = 0;
   float A[NV][8], B[NV][8], wp[NV][8], bp[NV][8];  // b g w_post, b g b_post, w_pre, b_pre
   if (P.y) {
     load_param<VEC, NV>(P.w_post, P.pdt, 1.0f, tid, group, dim, A);
@@ -194,12 +270,16 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_kernel(const __grid_constan
     load_param<VEC, NV>(P.b_pre, P.pdt, 0.0f, tid, group, dim, bp);
   }
   for (int64_t row = row0; row < P.rows; row += step) {
-    RowRegs<TS, VEC, NV> xr;
-    xr.load(static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
+    fetch(row + (P.slots - 1) * step, slot == 0 ? P.slots - 1 : slot - 1);
+    if (VEC) fetch_wait(P.slots - 1);
+    const char* here = mine + slot * slot_bytes;
+    if (++slot == P.slots) slot = 0;
+    RowS xr;
+    xr.load(here + at_x, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
     float r[NV][8];
     if (P.y) {
-      RowRegs<TB, VEC, NV> yr;
-      yr.load(static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+      RowB yr;
+      yr.load(here, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
       float v[NV][8];
 #pragma unroll
       for (int j = 0; j < NV; ++j) yr.w[j].unpack(v[j]);
@@ -237,137 +317,219 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_kernel(const __grid_constan
 // threads, S1 and P1 and (SUM0) S0 and P0, dim floats each.
 template <typename TS, typename TB, int VEC, int NV, bool LAYER, bool SUM0>
 __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_constant__ NormParams P) {
-  __shared__ float buf[2][32][4];
+  extern __shared__ char slots[];
+  __shared__ __align__(16) GroupBuf buf;
+  clear(buf);
+  typedef RowRegs<TS, VEC, NV> RowS;
+  typedef RowRegs<TB, VEC, NV> RowB;
   int half = 0, tid;
   const int64_t row0 = first_row(P, tid), step = (int64_t)gridDim.x * P.per_cta;
   const int group = P.group, dim = P.dim;
+  const int at_dz = RowB::bytes(group), at_r = 2 * at_dz, at_dr = at_r + RowS::bytes(group);
+  const int slot_bytes = at_dr + RowS::bytes(group);
+  char* mine = slots + (P.per_cta == 1 ? 0 : (threadIdx.x >> 5) * P.slots * slot_bytes);
+  auto fetch = [&](int64_t row, int slot) {
+    if (VEC) __syncwarp();  // the slot's last row has been read
+    if (VEC && row < P.rows) {
+      char* to = mine + slot * slot_bytes;
+      if (P.y) RowB::fetch(to, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+      if (P.pre) {
+        RowB::fetch(to + at_dz, static_cast<const TB*>(P.dz) + row * dim, tid, group, dim);
+        RowS::fetch(to + at_r, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
+      }
+      if (P.dr) RowS::fetch(to + at_dr, static_cast<const TS*>(P.dr) + row * dim, tid, group, dim);
+    }
+    if (VEC) fetched();
+  };
+  grid_go();
+  for (int s = 0; s + 1 < P.slots; ++s) fetch(row0 + s * step, s);
+  int slot = 0;
+  // For the gradient of a gate per token: the post norm's bias, read for every row.
+  float* bias = reinterpret_cast<float*>(slots + (VEC ? P.per_cta * P.slots * slot_bytes : 0));
+  if (P.bias) {
+    for (int c = threadIdx.x; c < dim; c += blockDim.x) bias[c] = param_at(P.b_post, c, P.pdt, 0.0f);
+    __syncthreads();
+  }
   const bool has_y = P.y != nullptr, token = P.gate_mode == DP_GATE_TOKEN;
-  float A[NV][8], wp[NV][8];  // b g w_post, w_pre
-  float S1[NV][8], P1[NV][8], S0[NV][8], P0[NV][8];
+  f2_t A[NV][4], wp[NV][4];  // b g w_post, w_pre
+  f2_t S1[NV][4], P1[NV][4], S0[NV][4], P0[NV][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) S1[j][k] = P1[j][k] = S0[j][k] = P0[j][k] = 0.0f;
-  if (has_y) {
-    load_param<VEC, NV>(P.w_post, P.pdt, 1.0f, tid, group, dim, A);
+    for (int k = 0; k < 4; ++k) A[j][k] = wp[j][k] = S1[j][k] = P1[j][k] = S0[j][k] = P0[j][k] = f2_both(0.0f);
+  {
+    float v[NV][8];
+    if (has_y) {
+      load_param<VEC, NV>(P.w_post, P.pdt, 1.0f, tid, group, dim, v);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int c = col_of<VEC>(tid, group, j, k);
+          v[j][k] *= P.gate_mode == DP_GATE_CHANNEL && c < dim ? P.b * param_at(P.gate, c, P.pdt, 1.0f) : P.b;
+          if (k & 1) A[j][k >> 1] = f2_pack(v[j][k - 1], v[j][k]);
+        }
+    }
+    if (P.pre) {
+      load_param<VEC, NV>(P.w_pre, P.pdt, 1.0f, tid, group, dim, v);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) wp[j][k] = f2_pack(v[j][2 * k], v[j][2 * k + 1]);
+    }
+  }
+  const float inv = 1.0f / (float)dim;
+  // The next row's statistics are loaded a row ahead, like its elements.
+  float2 next_pre = make_float2(0.0f, 1.0f), next_post = make_float2(0.0f, 1.0f);
+  uint32_t next_gate = P.pdt == DP_BF16 ? 0x3f80u : 0x3f800000u;  // as it lies in memory: a conversion would wait for it
+  auto scalars = [&](int64_t row) {
+    if (row >= P.rows) return;
+    if (P.pre) next_pre = P.pre_stats[row];
+    if (P.post) next_post = P.post_stats[row];
+    if (token) next_gate = P.pdt == DP_BF16 ? __ldg(static_cast<const uint16_t*>(P.gate) + row) : __ldg(static_cast<const uint32_t*>(P.gate) + row);
+  };
+  scalars(row0);
+
+  for (int64_t row = row0; row < P.rows; row += step) {
+    fetch(row + (P.slots - 1) * step, slot == 0 ? P.slots - 1 : slot - 1);
+    const float2 pre = next_pre, post = next_post;
+    const float gt = __uint_as_float(P.pdt == DP_BF16 ? next_gate << 16 : next_gate);
+    scalars(row + step);
+    if (VEC) fetch_wait(P.slots - 1);
+    const char* here = mine + slot * slot_bytes;
+    if (++slot == P.slots) slot = 0;
+    f2_t D[NV][4];
+    RowB yr;
+    if (has_y && !VEC) yr.load(here, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+    if (P.dr) {
+      RowS w;
+      w.load(here + at_dr, static_cast<const TS*>(P.dr) + row * dim, tid, group, dim);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) w.w[j].unpack2(D[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) D[j][k] = f2_both(0.0f);
+    }
+    if (P.pre) {
+      RowB zr;
+      RowS rr;
+      zr.load(here + at_dz, static_cast<const TB*>(P.dz) + row * dim, tid, group, dim);
+      rr.load(here + at_r, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
+      const f2_t less = f2_both(-pre.x), rstd = f2_both(pre.y);
+      f2_t v[NV][4], h[NV][4], s1 = f2_both(0.0f), s0 = f2_both(0.0f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        zr.w[j].unpack2(v[j]);
+        rr.w[j].unpack2(h[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (LAYER) h[j][k] = f2_add(h[j][k], less);
+          h[j][k] = f2_mul(h[j][k], rstd);
+          P1[j][k] = f2_fma(v[j][k], h[j][k], P1[j][k]);
+          if (SUM0) P0[j][k] = f2_add(P0[j][k], v[j][k]);
+          v[j][k] = f2_mul(v[j][k], wp[j][k]);  // zero beyond dim
+          s1 = f2_fma(v[j][k], h[j][k], s1);
+          if (LAYER) s0 = f2_add(s0, v[j][k]);
+        }
+      }
+      float s[LAYER ? 2 : 1] = {f2_sum(s1)};
+      if (LAYER) s[LAYER ? 1 : 0] = f2_sum(s0);
+      group_sum<LAYER ? 2 : 1>(s, group >> 5, buf, half);
+      const f2_t c1 = f2_both(-s[0] * inv), c0 = f2_both(LAYER ? -s[LAYER ? 1 : 0] * inv : 0.0f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f2_t x = f2_fma(h[j][k], c1, v[j][k]);
+          if (LAYER) x = f2_add(x, c0);
+          D[j][k] = f2_fma(x, rstd, D[j][k]);
+        }
+    }
+    if (has_y) {
+      if (VEC) yr.load(here, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+      const f2_t less = f2_both(-post.x), rstd = f2_both(post.y), gate = f2_both(gt);
+      f2_t v[NV][4], h[NV][4], s1 = f2_both(0.0f), s0 = f2_both(0.0f);
+      float s2 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        yr.w[j].unpack2(h[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (LAYER) h[j][k] = f2_add(h[j][k], less);
+          h[j][k] = f2_mul(h[j][k], rstd);
+          const f2_t q = f2_mul(gate, D[j][k]);
+          v[j][k] = f2_mul(A[j][k], D[j][k]);
+          S1[j][k] = f2_fma(q, h[j][k], S1[j][k]);
+          if (SUM0) S0[j][k] = f2_add(S0[j][k], q);
+          s1 = f2_fma(v[j][k], h[j][k], s1);
+          if (LAYER) s0 = f2_add(s0, v[j][k]);
+        }
+      }
+      if (P.bias) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int c = col_of<VEC>(tid, group, j, k);
+            float d[2];
+            f2_unpack(D[j][k >> 1], d[0], d[1]);
+            if (c < dim) s2 = fmaf(d[k & 1], bias[c], s2);
+          }
+      }
+      float c1 = f2_sum(s1), c0 = LAYER ? f2_sum(s0) : 0.0f;
+      if (token) {
+        float s[3] = {c1, c0, s2};
+        group_sum<3>(s, group >> 5, buf, half);
+        c1 = s[0];
+        c0 = s[1];
+        if (P.dgate_token && tid == 0) grad_put(P.dgate_token, row, P.pdt, P.accumulate, fmaf(P.b, s[2], s[0]));
+      } else if (P.post) {
+        float s[LAYER ? 2 : 1] = {c1};
+        if (LAYER) s[LAYER ? 1 : 0] = c0;
+        group_sum<LAYER ? 2 : 1>(s, group >> 5, buf, half);
+        c1 = s[0];
+        if (LAYER) c0 = s[LAYER ? 1 : 0];
+      }
+      const f2_t m1 = f2_both(P.post ? -c1 * inv : 0.0f), m0 = f2_both(P.post ? -c0 * inv : 0.0f), f = f2_both(gt * post.y);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f2_t x = f2_fma(h[j][k], m1, v[j][k]);
+          if (LAYER) x = f2_add(x, m0);
+          h[j][k] = f2_mul(x, f);
+        }
+      store_row2<TB, VEC, NV>(static_cast<TB*>(P.dy) + row * dim, tid, group, dim, h);
+    }
+    const f2_t a = f2_both(P.a);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) D[j][k] = f2_mul(D[j][k], a);
+    store_row2<TS, VEC, NV>(static_cast<TS*>(P.dx) + row * dim, tid, group, dim, D);
+  }
+  // One partial row a group of threads.
+  const int64_t part = (int64_t)blockIdx.x * P.per_cta + (P.per_cta == 1 ? 0 : threadIdx.x >> 5);
+  auto leave = [&](int which, const f2_t (&sum)[NV][4]) {
+    float* p = P.part + (part * (SUM0 ? 4 : 2) + which) * dim;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int c = col_of<VEC>(tid, group, j, k);
-        A[j][k] *= P.gate_mode == DP_GATE_CHANNEL && c < dim ? P.b * param_at(P.gate, c, P.pdt, 1.0f) : P.b;
+        float x[2];
+        f2_unpack(sum[j][k >> 1], x[0], x[1]);
+        if (c < dim) p[c] = x[k & 1];
       }
+  };
+  leave(0, S1);
+  leave(1, P1);
+  if (SUM0) {
+    leave(2, S0);
+    leave(3, P0);
   }
-  if (P.pre) load_param<VEC, NV>(P.w_pre, P.pdt, 1.0f, tid, group, dim, wp);
-  const float inv = 1.0f / (float)dim;
-
-  for (int64_t row = row0; row < P.rows; row += step) {
-    float D[NV][8];
-    RowRegs<TB, VEC, NV> yr;
-    if (has_y) yr.load(static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
-    if (P.dr) {
-      RowRegs<TS, VEC, NV> w;
-      w.load(static_cast<const TS*>(P.dr) + row * dim, tid, group, dim);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) w.w[j].unpack(D[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) D[j][k] = 0.0f;
-    }
-    if (P.pre) {
-      RowRegs<TB, VEC, NV> zr;
-      RowRegs<TS, VEC, NV> rr;
-      zr.load(static_cast<const TB*>(P.dz) + row * dim, tid, group, dim);
-      rr.load(static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
-      const float2 st = P.pre_stats[row];
-      float v[NV][8], h[NV][8], s[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        zr.w[j].unpack(v[j]);
-        rr.w[j].unpack(h[j]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          h[j][k] = (h[j][k] - st.x) * st.y;
-          P1[j][k] = fmaf(v[j][k], h[j][k], P1[j][k]);
-          if (SUM0) P0[j][k] += v[j][k];
-          v[j][k] *= wp[j][k];  // zero beyond dim
-          s[0] = fmaf(v[j][k], h[j][k], s[0]);
-          if (LAYER) s[1] += v[j][k];
-        }
-      }
-      if (LAYER) group_sum<2>(s, group >> 5, buf, half);
-      else {
-        float one[1] = {s[0]};
-        group_sum<1>(one, group >> 5, buf, half);
-        s[0] = one[0];
-      }
-      const float c1 = s[0] * inv, c0 = LAYER ? s[1] * inv : 0.0f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) D[j][k] = fmaf(st.y, fmaf(-h[j][k], c1, v[j][k]) - c0, D[j][k]);
-    }
-    if (has_y) {
-      const float2 st = P.post ? P.post_stats[row] : make_float2(0.0f, 1.0f);
-      const float gt = token ? param_at(P.gate, row, P.pdt, 1.0f) : 1.0f;
-      float h[NV][8], s[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        yr.w[j].unpack(h[j]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int c = col_of<VEC>(tid, group, j, k);
-          h[j][k] = (h[j][k] - st.x) * st.y;
-          const float q = gt * D[j][k], v = A[j][k] * D[j][k];
-          S1[j][k] = fmaf(q, h[j][k], S1[j][k]);
-          if (SUM0) S0[j][k] += q;
-          s[0] = fmaf(v, h[j][k], s[0]);
-          if (LAYER) s[1] += v;
-          if (token && P.b_post && c < dim) s[2] = fmaf(D[j][k], param_at(P.b_post, c, P.pdt, 0.0f), s[2]);
-        }
-      }
-      if (P.post || token) {
-        if (LAYER || token) group_sum<3>(s, group >> 5, buf, half);
-        else {
-          float one[1] = {s[0]};
-          group_sum<1>(one, group >> 5, buf, half);
-          s[0] = one[0];
-        }
-      }
-      if (token && P.dgate_token && tid == 0)
-        grad_put(P.dgate_token, row, P.pdt, P.accumulate, fmaf(P.b, s[2], s[0]));
-      const float c1 = P.post ? s[0] * inv : 0.0f, c0 = P.post && LAYER ? s[1] * inv : 0.0f, f = gt * st.y;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[j][k] = f * (fmaf(-h[j][k], c1, A[j][k] * D[j][k]) - c0);
-      store_row<TB, VEC, NV>(static_cast<TB*>(P.dy) + row * dim, tid, group, dim, h);
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) D[j][k] *= P.a;
-    store_row<TS, VEC, NV>(static_cast<TS*>(P.dx) + row * dim, tid, group, dim, D);
-  }
-  // One partial row a group of threads.
-  const int64_t part = (int64_t)blockIdx.x * P.per_cta + (P.per_cta == 1 ? 0 : threadIdx.x >> 5);
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = col_of<VEC>(tid, group, j, k);
-      if (c < dim) {
-        float* p = P.part + part * (SUM0 ? 4 : 2) * dim + c;
-        p[0] = S1[j][k];
-        p[dim] = P1[j][k];
-        if (SUM0) {
-          p[2 * (int64_t)dim] = S0[j][k];
-          p[3 * (int64_t)dim] = P0[j][k];
-        }
-      }
-    }
 }
 
 struct FinishParams {
@@ -379,13 +541,14 @@ struct FinishParams {
   float b;
 };
 
-// Adds the partial rows of 32 columns in 16 interleaved parts, then the parts in order.
+// Adds the partial rows of 16 columns in 64 interleaved parts, then the parts in order.
 __global__ void __launch_bounds__(FIN_COLS* FIN_ROWS) norm_finish_kernel(const __grid_constant__ FinishParams P) {
   __shared__ float sums[FIN_ROWS][4][FIN_COLS];
+  grid_wait();
   const int c = blockIdx.x * FIN_COLS + threadIdx.x;
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < P.dim) {
-#pragma unroll 4
+#pragma unroll 5
     for (int64_t i = threadIdx.y; i < P.parts; i += FIN_ROWS) {
       const float* p = P.part + i * (P.sum0 ? 4 : 2) * P.dim + c;
       s[0] += p[0];
@@ -430,26 +593,61 @@ Shape shape_of(int dim) {
   return s;
 }
 
+// Rows in flight, and with that the shared memory, of a kernel whose CTAs take `set` bytes a row: four where all CTAs that the
+// registers allow an SM still fit, fewer for long rows.  A kernel's last answer is kept: asking takes longer than a launch.
+struct Plan1 {
+  int device = -1, threads = 0, slots = 1, ctas = 0;  // ctas: one wave
+  int64_t set = -1, more = -1;
+};
 template <typename K>
-int norm_grid(K kernel, const Shape& s, int64_t rows, int most) {
-  const int64_t want = (rows + s.per_cta - 1) / s.per_cta;
-  const int g = occupancy_grid(kernel, s.threads, 0, want < most ? (int)want : most);
-  return g;
+void plan_of(K kernel, int threads, int64_t set, int64_t more, Plan1& c) {
+  int device = 0;
+  cudaGetDevice(&device);
+  if (c.device == device && c.threads == threads && c.set == set && c.more == more) return;
+  c.slots = 1;
+  int per_sm = 1;
+  if (set > 0) {
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+    const int64_t room = 220 * 1024;
+    if (per_sm < 1) per_sm = 1;
+    while (per_sm > 1 && per_sm * (set * 2 + more) > room) --per_sm;
+    const int64_t n = (room / per_sm - more) / set;
+    c.slots = (int)(n < 1 ? 1 : n > MAX_SLOTS ? MAX_SLOTS : n);
+  }
+  const size_t smem = (size_t)(c.slots * set + more);
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  c.ctas = occupancy_grid(kernel, threads, smem, INT32_MAX);
+  c.device = device;
+  c.threads = threads;
+  c.set = set;
+  c.more = more;
+}
+template <typename K>
+int launch_rows(K kernel, Plan1& c, const Shape& s, NormParams& P, int64_t set, int64_t more, int most, cudaStream_t stream) {
+  plan_of(kernel, s.threads, set, more, c);
+  P.slots = c.slots;
+  const int64_t want = (P.rows + s.per_cta - 1) / s.per_cta;
+  int64_t grid = want < c.ctas ? want : c.ctas;
+  if (grid > most) grid = most;
+  kernel<<<(unsigned)grid, s.threads, (size_t)(c.slots * set + more), stream>>>(P);
+  return (int)grid;
 }
 
 template <typename TS, typename TB, int VEC, int NV>
-void run_forward(const NormParams& P, const Shape& s, cudaStream_t stream) {
-  auto k = norm_kernel<TS, TB, VEC, NV>;
-  k<<<norm_grid(k, s, P.rows, INT32_MAX), s.threads, 0, stream>>>(P);
+void run_forward(NormParams P, const Shape& s, cudaStream_t stream) {
+  static thread_local Plan1 plan;
+  launch_rows(norm_kernel<TS, TB, VEC, NV>, plan, s, P, VEC ? (int64_t)s.threads * NV * 8 * (sizeof(TS) + sizeof(TB)) : 0, 0,
+              INT32_MAX, stream);
 }
 template <typename TS, typename TB, int VEC, int NV>
-int run_grad(const NormParams& P, const Shape& s, bool sum0, cudaStream_t stream) {
+int run_grad(NormParams P, const Shape& s, bool sum0, cudaStream_t stream) {
+  static thread_local Plan1 plan[3];
+  const int which = P.layer ? 2 : sum0 ? 1 : 0;
   auto k = P.layer ? norm_grad_kernel<TS, TB, VEC, NV, true, true>
            : sum0  ? norm_grad_kernel<TS, TB, VEC, NV, false, true>
                    : norm_grad_kernel<TS, TB, VEC, NV, false, false>;
-  const int grid = norm_grid(k, s, P.rows, MAX_PARTS / s.per_cta);
-  k<<<grid, s.threads, 0, stream>>>(P);
-  return grid * s.per_cta;
+  return s.per_cta * launch_rows(k, plan[which], s, P, VEC ? (int64_t)s.threads * NV * 8 * 2 * (sizeof(TS) + sizeof(TB)) : 0,
+                                 P.bias ? P.dim * 4 : 0, MAX_PARTS / s.per_cta, stream);
 }
 
 // f(stream type, block type, VEC, NV) for the sizes and types of one call.
@@ -530,6 +728,11 @@ NormParams base_params(const dp_block_norm_t& p, const Shape& s) {
   return P;
 }
 
+// Whether one row of a CTA fits its shared memory (`pairs` rows of the stream and of the block).
+bool slots_fit(const dp_block_norm_t& p, const Shape& s, int pairs) {
+  return (int64_t)s.threads * s.nv * 8 * pairs * (elem_size(p.stream_dtype) + elem_size(p.block_dtype)) + 4 * p.dim <= 220 * 1024;
+}
+
 bool all16(std::initializer_list<const void*> ps) {
   for (const void* q : ps)
     if (!is_aligned(q, 16)) return false;
@@ -578,7 +781,7 @@ dp_status_t dp_block_norm(const dp_block_norm_t* p, void* r, void* z, const void
   P.post_stats = reinterpret_cast<float2*>(post_stats);
   P.pre_stats = reinterpret_cast<float2*>(pre_stats);
   NvtxRange range("block norm");
-  dispatch(*p, p->dim % 8 == 0 && all16({x, y, r, z}), s.nv, Forward{P, s, (cudaStream_t)stream});
+  dispatch(*p, p->dim % 8 == 0 && slots_fit(*p, s, 1) && all16({x, y, r, z}), s.nv, Forward{P, s, (cudaStream_t)stream});
   return op_launched("block norm launch", 1);
 }
 
@@ -643,7 +846,8 @@ dp_status_t dp_block_norm_grad(const dp_block_norm_t* p, void* dx, void* dy, con
     P.pre_stats = reinterpret_cast<float2*>(const_cast<float*>(pre_stats));
     P.dgate_token = p->gate_mode == DP_GATE_TOKEN ? dgate : nullptr;
     P.part = static_cast<float*>(ws);
-    parts = dispatch(*p, p->dim % 8 == 0 && all16({dx, dy, dr, dz, r, y}), s.nv, Gradient{P, s, sum0, stream});
+    P.bias = P.dgate_token && P.b_post;
+    parts = dispatch(*p, p->dim % 8 == 0 && slots_fit(*p, s, 2) && all16({dx, dy, dr, dz, r, y}), s.nv, Gradient{P, s, sum0, stream});
     ++launches;
   }
   FinishParams F = {};
@@ -664,7 +868,8 @@ dp_status_t dp_block_norm_grad(const dp_block_norm_t* p, void* dx, void* dy, con
   F.db_pre = db_pre;
   F.b = p->branch_scale;
   if (F.dw_post || F.db_post || F.dgate || F.dw_pre || F.db_pre) {
-    norm_finish_kernel<<<(p->dim + FIN_COLS - 1) / FIN_COLS, dim3(FIN_COLS, FIN_ROWS), 0, stream>>>(F);
+    const cudaError_t e = launch_after(norm_finish_kernel, (p->dim + FIN_COLS - 1) / FIN_COLS, dim3(FIN_COLS, FIN_ROWS), stream, F);
+    if (e != cudaSuccess) return op_fail(DP_ERR_CUDA, "block norm gradient launch: %s", cudaGetErrorString(e));
     ++launches;
   }
   return launches ? op_launched("block norm gradient launch", launches) : DP_OK;
