@@ -7,8 +7,10 @@
 //
 // Everything here is elementwise and bounded by memory: for a gated activation the forward reads 4 bytes and writes
 // 2 + 2 (1 + 1/32) an element, the gradient reads 2 + 2 (1 + 1/32) and writes 6 -- against 6 read and 6 written from
-// bf16 copies, and the saved bytes are the point: a third of the memory between the passes is gone.  A thread takes eight
-// consecutive elements (16 bytes of bf16, 8 of codes); four neighbours make a group and find its maximum by two shuffles.
+// bf16 copies, and the saved bytes are the point: a third of the memory between the passes is gone.  A thread takes pieces of
+// eight consecutive elements (16 bytes of bf16, 8 of codes), all of a thread's loads in flight at once; four neighbours make a
+// group and find its maximum by two shuffles.  Instructions count nearly as much as bytes: conversions between codes and floats
+// go by the fraction of a float near 2^23 and byte permutes, not by conversion instructions, and fp32 is done in pairs.
 #include "op_common.cuh"
 
 namespace dp {
@@ -30,33 +32,52 @@ __device__ __forceinline__ float step_of(uint32_t E) { return E == 255u ? __uint
 // 1 / step: exact, and normal for E <= 253 (no group has more than 249).
 __device__ __forceinline__ float inv_step_of(uint32_t E) { return __uint_as_float((254u - E) << 23); }
 
-// Codes of eight values, the group's byte known.
-__device__ __forceinline__ uint2 codes_of(const float (&v)[8], uint32_t E) {
+// Codes of eight values (as pairs), the group's byte known: x / step + 1.5 2^23 has the rounded quotient in its low bits, in two's
+// complement (the product is exact, so ties go to even as they should).
+__device__ __forceinline__ uint32_t low_bytes(f2_t a, f2_t b) {
+  const uint32_t x = __byte_perm((uint32_t)a, (uint32_t)(a >> 32), 0x0040), y = __byte_perm((uint32_t)b, (uint32_t)(b >> 32), 0x0040);
+  return __byte_perm(x, y, 0x5410);
+}
+__device__ __forceinline__ uint2 codes_of(const f2_t (&v)[4], uint32_t E) {
   if (E == 255u) return make_uint2(0u, 0u);
-  const float s = inv_step_of(E);
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int k = 0; k < 8; ++k) w[k >> 2] |= ((uint32_t)__float2int_rn(v[k] * s) & 0xffu) << (8 * (k & 3));
-  return make_uint2(w[0], w[1]);
+  const f2_t s = f2_both(inv_step_of(E)), m = f2_both(12582912.0f);
+  return make_uint2(low_bytes(f2_fma(v[0], s, m), f2_fma(v[1], s, m)), low_bytes(f2_fma(v[2], s, m), f2_fma(v[3], s, m)));
 }
-__device__ __forceinline__ void values_of(uint2 c, uint32_t E, float (&v)[8]) {
-  const float s = step_of(E);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = (float)(int8_t)(((k < 4 ? c.x : c.y) >> (8 * (k & 3))) & 0xffu) * s;
+// A code c as the float 2^23 + 128 + c, whose low byte is c's with the top bit turned.
+__device__ __forceinline__ f2_t two_codes(uint32_t turned, uint32_t which) {
+  const uint32_t lo = __byte_perm(turned, 0x4b000000u, 0x7440 + which), hi = __byte_perm(turned, 0x4b000000u, 0x7441 + which);
+  return f2_add(f2_pack(__uint_as_float(lo), __uint_as_float(hi)), f2_both(-8388736.0f));
 }
-
-// Largest magnitude of the group that this thread and its three neighbours hold.  fmaxf drops a NaN, so one is carried
-// as an infinity.
-__device__ __forceinline__ float group_top(const float (&v)[8]) {
-  float m = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m = fmaxf(m, nonfinite(v[k]) ? __uint_as_float(0x7f800000u) : fabsf(v[k]));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+__device__ __forceinline__ void values_of(uint2 c, uint32_t E, f2_t (&v)[4]) {
+  const f2_t s = f2_both(step_of(E));
+  const uint32_t a = c.x ^ 0x80808080u, b = c.y ^ 0x80808080u;
+  v[0] = f2_mul(two_codes(a, 0), s);
+  v[1] = f2_mul(two_codes(a, 2), s);
+  v[2] = f2_mul(two_codes(b, 0), s);
+  v[3] = f2_mul(two_codes(b, 2), s);
 }
 
-// Where a thread's eight elements lie.  Elements are numbered through the padded rows, so a group never leaves a warp's
-// aligned quad of threads; a CTA finds its first row by one 64-bit division.
+// Largest magnitude of the group that this thread and its three neighbours hold, as bits: infinities and NaNs come out above
+// all finite values.
+__device__ __forceinline__ float group_top(uint32_t m) {
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return __uint_as_float(max(m, __shfl_xor_sync(0xffffffffu, m, 2)));
+}
+__device__ __forceinline__ uint32_t top_of(const Raw8<bf16_t>& w) {  // two bf16 at a time
+  const uint32_t k = 0x7fff7fffu;
+  const uint32_t m = __vmaxu2(__vmaxu2(w.a.x & k, w.a.y & k), __vmaxu2(w.a.z & k, w.a.w & k));
+  return max(m << 16, m & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t top_of(const Raw8<float>& w) {
+  const uint32_t k = 0x7fffffffu;
+  const float4 a = w.a, b = w.b;
+  const uint32_t x = max(max(__float_as_uint(a.x) & k, __float_as_uint(a.y) & k), max(__float_as_uint(a.z) & k, __float_as_uint(a.w) & k));
+  const uint32_t y = max(max(__float_as_uint(b.x) & k, __float_as_uint(b.y) & k), max(__float_as_uint(b.z) & k, __float_as_uint(b.w) & k));
+  return max(x, y);
+}
+
+// Where a thread's pieces lie.  Pieces are numbered through the padded rows, so a group never leaves a warp's aligned quad of
+// threads.  A CTA takes U times 256 consecutive pieces, and finds its first row by one 64-bit division.
 struct Place {
   int64_t row;
   int col;
@@ -67,77 +88,107 @@ struct Walk {
   int pieces;  // eights of a padded row
   int dim;
 };
-__device__ __forceinline__ Place place_of(const Walk& W) {
-  const int64_t first = (int64_t)blockIdx.x * THREADS;
+template <int U>
+__device__ __forceinline__ void places_of(const Walk& W, Place (&p)[U]) {
+  const int64_t first = (int64_t)blockIdx.x * (THREADS * U);
   const int64_t row0 = first / W.pieces;
   const uint32_t rest = (uint32_t)(first - row0 * W.pieces) + threadIdx.x;
-  const uint32_t down = rest / (uint32_t)W.pieces;
-  Place p;
-  p.row = row0 + down;
-  p.col = (int)(rest - down * (uint32_t)W.pieces) * 8;
-  p.on = p.row < W.rows;
-  return p;
-}
-
-template <typename T>
-__device__ __forceinline__ void load_piece(const T* base, int64_t ld, const Place& p, int dim, int vec, float (&v)[8]) {
-  const T* q = base + p.row * ld + p.col;
-  if (p.on && vec && p.col < dim) {  // vec: dim is a multiple of 8
-    const Raw8<T> w = load_raw8(q);
-    w.unpack(v);
-  } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = p.on && p.col + k < dim ? Elem<T>::get(q[k]) : 0.0f;
+  for (int i = 0; i < U; ++i) {
+    const uint32_t at = rest + i * THREADS, down = at / (uint32_t)W.pieces;
+    p[i].row = row0 + down;
+    p[i].col = (int)(at - down * (uint32_t)W.pieces) * 8;
+    p[i].on = p[i].row < W.rows;
   }
 }
+
+// Pieces that are not there, or lie beyond the row's end, are zeros.  vec: dim is a multiple of 8 and rows 16-byte aligned.
 template <typename T>
-__device__ __forceinline__ void store_piece(T* base, int64_t ld, const Place& p, int dim, int vec, const float (&v)[8]) {
+__device__ __forceinline__ Raw8<T> load_piece(const T* base, int64_t ld, const Place& p, int dim, int vec) {
+  const T* q = base + p.row * ld + p.col;
+  if (p.on && vec && p.col < dim) return load_raw8(q);
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (p.on && !vec) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (p.col + k < dim) v[k] = Elem<T>::get(q[k]);
+  }
+  Raw8<T> w;
+  w.pack(v);
+  return w;
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* base, int64_t ld, const Place& p, int dim, int vec, const f2_t (&v)[4]) {
   T* q = base + p.row * ld + p.col;
   if (!p.on) return;
   if (vec) {
     if (p.col >= dim) return;
     Raw8<T> o;
-    o.pack(v);
+    o.pack2(v);
     store_raw8(q, o);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (p.col + k < dim) q[k] = Elem<T>::put(v[k]);
+    for (int k = 0; k < 8; ++k) {
+      float x[2];
+      f2_unpack(v[k >> 1], x[0], x[1]);
+      if (p.col + k < dim) q[k] = Elem<T>::put(x[k & 1]);
+    }
   }
 }
 struct Ckpt {
   int8_t* codes;
   uint8_t* scales;
 };
-__device__ __forceinline__ void put_ckpt(const Ckpt& c, const Place& p, int pitch, const float (&v)[8]) {
-  const uint32_t E = step_byte(group_top(v));
+template <typename T>
+__device__ __forceinline__ void put_ckpt(const Ckpt& c, const Place& p, int pitch, const Raw8<T>& w, const f2_t (&v)[4]) {
+  const uint32_t E = step_byte(group_top(top_of(w)));
   if (!p.on) return;
   *reinterpret_cast<uint2*>(c.codes + p.row * pitch + p.col) = codes_of(v, E);
   if ((p.col & (GROUP - 1)) == 0) c.scales[p.row * (pitch / GROUP) + p.col / GROUP] = (uint8_t)E;
 }
-__device__ __forceinline__ void get_ckpt(const Ckpt& c, const Place& p, int pitch, float (&v)[8]) {
-  uint2 w = make_uint2(0u, 0u);
-  uint32_t E = 1u;
+struct Kept {  // a piece of a checkpoint
+  uint2 codes;
+  uint32_t E;
+};
+__device__ __forceinline__ Kept get_ckpt(const Ckpt& c, const Place& p, int pitch) {
+  Kept k = {make_uint2(0u, 0u), 1u};
   if (p.on) {
-    w = __ldcs(reinterpret_cast<const uint2*>(c.codes + p.row * pitch + p.col));
-    E = c.scales[p.row * (pitch / GROUP) + p.col / GROUP];
+    k.codes = __ldcs(reinterpret_cast<const uint2*>(c.codes + p.row * pitch + p.col));
+    k.E = c.scales[p.row * (pitch / GROUP) + p.col / GROUP];
   }
-  values_of(w, E, v);
+  return k;
 }
+
+constexpr int COPY_U = 4, ACT_U = 2;  // pieces of a thread
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS) encode_kernel(Ckpt c, const T* x, int64_t ldx, Walk W, int vec) {
-  const Place p = place_of(W);
-  float v[8];
-  load_piece(x, ldx, p, W.dim, vec, v);
-  put_ckpt(c, p, W.pieces * 8, v);
+  Place p[COPY_U];
+  Raw8<T> w[COPY_U];
+  places_of(W, p);
+#pragma unroll
+  for (int i = 0; i < COPY_U; ++i) w[i] = load_piece(x, ldx, p[i], W.dim, vec);
+#pragma unroll
+  for (int i = 0; i < COPY_U; ++i) {
+    f2_t v[4];
+    w[i].unpack2(v);
+    put_ckpt(c, p[i], W.pieces * 8, w[i], v);
+  }
 }
 template <typename T>
 __global__ void __launch_bounds__(THREADS) decode_kernel(T* x, int64_t ldx, Ckpt c, Walk W, int vec) {
-  const Place p = place_of(W);
-  float v[8];
-  get_ckpt(c, p, W.pieces * 8, v);
-  store_piece(x, ldx, p, W.dim, vec, v);
+  grid_go();  // a product of the decoded rows may be set up meanwhile
+  Place p[COPY_U];
+  Kept k[COPY_U];
+  places_of(W, p);
+#pragma unroll
+  for (int i = 0; i < COPY_U; ++i) k[i] = get_ckpt(c, p[i], W.pieces * 8);
+#pragma unroll
+  for (int i = 0; i < COPY_U; ++i) {
+    f2_t v[4];
+    values_of(k[i].codes, k[i].E, v);
+    store_piece(x, ldx, p[i], W.dim, vec, v);
+  }
 }
 
 // f(g) and f'(g), with s the logistic function.  SiLU: f = g s(g), f' = s (1 + g (1 - s)).  GELU's tanh form is
@@ -170,39 +221,69 @@ __device__ __forceinline__ void act_of(float g, float& f, float& df) {
 template <int ACT, bool GATED>
 __global__ void __launch_bounds__(THREADS) act_kernel(bf16_t* h, const bf16_t* g, const bf16_t* u, Ckpt g8, Ckpt u8,
                                                       int64_t ld, int64_t ldh, Walk W, int vec) {
-  const Place p = place_of(W);
-  float gv[8], uv[8], f, df;
-  load_piece(g, ld, p, W.dim, vec, gv);
-  if (GATED) load_piece(u, ld, p, W.dim, vec, uv);
-  put_ckpt(g8, p, W.pieces * 8, gv);
-  if (GATED) put_ckpt(u8, p, W.pieces * 8, uv);
+  Place p[ACT_U];
+  Raw8<bf16_t> gw[ACT_U], uw[ACT_U];
+  places_of(W, p);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    act_of<ACT>(gv[k], f, df);
-    gv[k] = GATED ? f * uv[k] : f;
+  for (int i = 0; i < ACT_U; ++i) {
+    gw[i] = load_piece(g, ld, p[i], W.dim, vec);
+    if (GATED) uw[i] = load_piece(u, ld, p[i], W.dim, vec);
   }
-  store_piece(h, ldh, p, W.dim, vec, gv);
+#pragma unroll
+  for (int i = 0; i < ACT_U; ++i) {
+    f2_t gv[4], uv[4];
+    gw[i].unpack2(gv);
+    put_ckpt(g8, p[i], W.pieces * 8, gw[i], gv);
+    if (GATED) {
+      uw[i].unpack2(uv);
+      put_ckpt(u8, p[i], W.pieces * 8, uw[i], uv);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float a, b, fa, fb, unused;
+      f2_unpack(gv[k], a, b);
+      act_of<ACT>(a, fa, unused);
+      act_of<ACT>(b, fb, unused);
+      gv[k] = GATED ? f2_mul(f2_pack(fa, fb), uv[k]) : f2_pack(fa, fb);
+    }
+    store_piece(h, ldh, p[i], W.dim, vec, gv);
+  }
 }
 
 template <int ACT, bool GATED>
 __global__ void __launch_bounds__(THREADS) act_grad_kernel(bf16_t* dg, bf16_t* du, bf16_t* h, const bf16_t* dh, Ckpt g8,
                                                            Ckpt u8, int64_t ld, int64_t ldh, Walk W, int vec) {
-  const Place p = place_of(W);
-  float dv[8], gv[8], uv[8], hv[8];
-  load_piece(dh, ldh, p, W.dim, vec, dv);
-  get_ckpt(g8, p, W.pieces * 8, gv);
-  if (GATED) get_ckpt(u8, p, W.pieces * 8, uv);
+  Place p[ACT_U];
+  Raw8<bf16_t> dw[ACT_U];
+  Kept gk[ACT_U], uk[ACT_U];
+  places_of(W, p);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float f, df;
-    act_of<ACT>(gv[k], f, df);
-    hv[k] = GATED ? f * uv[k] : f;
-    gv[k] = (GATED ? dv[k] * uv[k] : dv[k]) * df;
-    dv[k] *= f;
+  for (int i = 0; i < ACT_U; ++i) {
+    dw[i] = load_piece(dh, ldh, p[i], W.dim, vec);
+    gk[i] = get_ckpt(g8, p[i], W.pieces * 8);
+    if (GATED) uk[i] = get_ckpt(u8, p[i], W.pieces * 8);
   }
-  store_piece(dg, ld, p, W.dim, vec, gv);
-  if (GATED) store_piece(du, ld, p, W.dim, vec, dv);
-  if (h) store_piece(h, ldh, p, W.dim, vec, hv);
+#pragma unroll
+  for (int i = 0; i < ACT_U; ++i) {
+    f2_t dv[4], gv[4], uv[4], hv[4];
+    dw[i].unpack2(dv);
+    values_of(gk[i].codes, gk[i].E, gv);
+    if (GATED) values_of(uk[i].codes, uk[i].E, uv);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float a, b, fa, fb, da, db;
+      f2_unpack(gv[k], a, b);
+      act_of<ACT>(a, fa, da);
+      act_of<ACT>(b, fb, db);
+      const f2_t f = f2_pack(fa, fb), df = f2_pack(da, db);
+      hv[k] = GATED ? f2_mul(f, uv[k]) : f;
+      gv[k] = f2_mul(GATED ? f2_mul(dv[k], uv[k]) : dv[k], df);
+      dv[k] = f2_mul(dv[k], f);
+    }
+    store_piece(dg, ld, p[i], W.dim, vec, gv);
+    if (GATED) store_piece(du, ld, p[i], W.dim, vec, dv);
+    if (h) store_piece(h, ldh, p[i], W.dim, vec, hv);
+  }
 }
 
 // ---------------------------------------------------------------------------------------------------- host side
@@ -224,7 +305,7 @@ dp_status_t check_ckpt(const int8_t* codes, const uint8_t* scales, bool needed, 
   return DP_OK;
 }
 Walk walk_of(int64_t rows, int64_t dim) { return Walk{rows, (int)(dp_ckpt8_pitch(dim) / 8), (int)dim}; }
-unsigned grid_of(const Walk& W) { return (unsigned)((W.rows * W.pieces + THREADS - 1) / THREADS); }
+unsigned grid_of(const Walk& W, int u) { return (unsigned)((W.rows * W.pieces + THREADS * u - 1) / (THREADS * u)); }
 bool rows16(const void* p, int64_t ld, int size) { return is_aligned(p, 16) && ld * size % 16 == 0; }
 
 }  // namespace
@@ -249,9 +330,9 @@ dp_status_t dp_ckpt8_encode(int8_t* codes, uint8_t* scales, const void* x, int64
   const int vec = dim % 8 == 0 && rows16(x, ldx, e);
   NvtxRange range("checkpoint encode");
   if (dtype == DP_BF16)
-    encode_kernel<<<grid_of(W), THREADS, 0, (cudaStream_t)stream>>>(Ckpt{codes, scales}, (const bf16_t*)x, ldx, W, vec);
+    encode_kernel<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>(Ckpt{codes, scales}, (const bf16_t*)x, ldx, W, vec);
   else
-    encode_kernel<<<grid_of(W), THREADS, 0, (cudaStream_t)stream>>>(Ckpt{codes, scales}, (const float*)x, ldx, W, vec);
+    encode_kernel<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>(Ckpt{codes, scales}, (const float*)x, ldx, W, vec);
   return op_launched("checkpoint encode launch", 1);
 }
 
@@ -269,9 +350,9 @@ dp_status_t dp_ckpt8_decode(void* x, const int8_t* codes, const uint8_t* scales,
   const int vec = dim % 8 == 0 && rows16(x, ldx, e);
   NvtxRange range("checkpoint decode");
   if (dtype == DP_BF16)
-    decode_kernel<<<grid_of(W), THREADS, 0, (cudaStream_t)stream>>>((bf16_t*)x, ldx, c, W, vec);
+    decode_kernel<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>((bf16_t*)x, ldx, c, W, vec);
   else
-    decode_kernel<<<grid_of(W), THREADS, 0, (cudaStream_t)stream>>>((float*)x, ldx, c, W, vec);
+    decode_kernel<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>((float*)x, ldx, c, W, vec);
   return op_launched("checkpoint decode launch", 1);
 }
 
@@ -295,7 +376,7 @@ dp_status_t dp_act_ckpt8(uint16_t* h, const uint16_t* g, const uint16_t* u, int8
   auto k = act == DP_ACT_SILU ? (u ? act_kernel<DP_ACT_SILU, true> : act_kernel<DP_ACT_SILU, false>)
                               : (u ? act_kernel<DP_ACT_GELU, true> : act_kernel<DP_ACT_GELU, false>);
   NvtxRange range("activation with checkpoint");
-  k<<<grid_of(W), THREADS, 0, (cudaStream_t)stream>>>(h, g, u, a, b, ld, ldh, W, vec);
+  k<<<grid_of(W, ACT_U), THREADS, 0, (cudaStream_t)stream>>>(h, g, u, a, b, ld, ldh, W, vec);
   return op_launched("activation launch", 1);
 }
 
@@ -321,7 +402,7 @@ dp_status_t dp_act_ckpt8_grad(uint16_t* dg, uint16_t* du, uint16_t* h, const uin
   auto k = act == DP_ACT_SILU ? (u8 ? act_grad_kernel<DP_ACT_SILU, true> : act_grad_kernel<DP_ACT_SILU, false>)
                               : (u8 ? act_grad_kernel<DP_ACT_GELU, true> : act_grad_kernel<DP_ACT_GELU, false>);
   NvtxRange range("activation gradient");
-  k<<<grid_of(W), THREADS, 0, (cudaStream_t)stream>>>(dg, du, h, dh, a, b, ld, ldh, W, vec);
+  k<<<grid_of(W, ACT_U), THREADS, 0, (cudaStream_t)stream>>>(dg, du, h, dh, a, b, ld, ldh, W, vec);
   return op_launched("activation gradient launch", 1);
 }
 

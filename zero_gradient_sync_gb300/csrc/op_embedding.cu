@@ -565,9 +565,15 @@ dp_status_t check_ids(const void* ids, int64_t tokens, int id_bits) {
 
 template <int CTAS>
 cudaError_t launch_sort(const SortParams& S, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(emb_sort_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SortSmem));
-  if (e == cudaSuccess && CTAS > 8) e = cudaFuncSetAttribute(emb_sort_kernel<CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
+  static thread_local int ready = -1;  // the device whose kernel has its shared memory and cluster size granted
+  int device = 0;
+  cudaGetDevice(&device);
+  if (ready != device) {
+    cudaError_t e = cudaFuncSetAttribute(emb_sort_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SortSmem));
+    if (e == cudaSuccess && CTAS > 8) e = cudaFuncSetAttribute(emb_sort_kernel<CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    ready = device;
+  }
   const int64_t want = (S.fill_bytes + SORT_THREADS * 16 * 4 - 1) / (SORT_THREADS * 16 * 4);
   const int64_t most = (int64_t)sm_count() * 2;
   const int64_t fill_ctas = ((want < most ? want : most) + CTAS - 1) / CTAS * CTAS;

@@ -153,6 +153,21 @@ __device__ __forceinline__ void store_row2(T* row, int tid, int group, int dim, 
 template <int VEC, int NV>
 __device__ __forceinline__ void load_param(const void* p, int dtype, float none, int tid, int group, int dim,
                                            float (&v)[NV][8]) {
+  if (VEC && p && ((uintptr_t)p & 15) == 0) {  // whole pieces as 16-byte words
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = col_of<1>(tid, group, j, 0);
+      if (c >= dim) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
+      } else if (dtype == DP_BF16) {
+        load_raw8(static_cast<const bf16_t*>(p) + c).unpack(v[j]);
+      } else {
+        load_raw8(static_cast<const float*>(p) + c).unpack(v[j]);
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -192,30 +207,44 @@ __device__ __forceinline__ void clear(GroupBuf& buf) {
   __syncthreads();
 }
 
-// Mean (0 for RMS) and 1 / sqrt(var + eps) of a row held in registers.  Pieces beyond dim hold zeros.
-template <int VEC, int NV>
-__device__ __forceinline__ float2 row_stats(const float (&v)[NV][8], int layer, float eps, int tid, int group, int dim,
-                                            GroupBuf& buf, int& half) {
-  float mean = 0.0f, s[1];
-  if (layer) {
-    s[0] = 0.0f;
+// Mean (0 for RMS) and 1 / sqrt(var + eps) of a row held in registers, which is centred on the way.  Pieces beyond dim hold
+// zeros, before and after.
+template <int VEC, int NV, bool LAYER>
+__device__ __forceinline__ float2 row_stats(f2_t (&v)[NV][4], float eps, float inv, int tid, int group, int dim, GroupBuf& buf,
+                                            int& half) {
+  float s[1], mean = 0.0f;
+  f2_t sum = f2_both(0.0f);
+  if (LAYER) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s[0] += v[j][k];
+      for (int k = 0; k < 4; ++k) sum = f2_add(sum, v[j][k]);
+    s[0] = f2_sum(sum);
     group_sum<1>(s, group >> 5, buf, half);
-    mean = s[0] / (float)dim;
+    mean = s[0] * inv;
+    const f2_t less = f2_both(-mean);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (VEC) {
+          if (col_of<1>(tid, group, j, 0) < dim) v[j][k] = f2_add(v[j][k], less);
+        } else {
+          float a, b;
+          f2_unpack(v[j][k], a, b);
+          v[j][k] = f2_pack(col_of<0>(tid, group, j, 2 * k) < dim ? a - mean : 0.0f,
+                            col_of<0>(tid, group, j, 2 * k + 1) < dim ? b - mean : 0.0f);
+        }
+      }
+    sum = f2_both(0.0f);
   }
-  s[0] = 0.0f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float d = col_of<VEC>(tid, group, j, k) < dim ? v[j][k] - mean : 0.0f;
-      s[0] = fmaf(d, d, s[0]);
-    }
+    for (int k = 0; k < 4; ++k) sum = f2_fma(v[j][k], v[j][k], sum);
+  s[0] = f2_sum(sum);
   group_sum<1>(s, group >> 5, buf, half);
-  return make_float2(mean, 1.0f / sqrtf(s[0] / (float)dim + eps));
+  return make_float2(mean, 1.0f / sqrtf(fmaf(s[0], inv, eps)));
 }
 
 // Which row a group of threads starts with, and the step between its rows.
@@ -228,8 +257,9 @@ __device__ __forceinline__ int64_t first_row(const NormParams& P, int& tid) {
   return (int64_t)blockIdx.x * P.per_cta + (threadIdx.x >> 5);
 }
 
-template <typename TS, typename TB, int VEC, int NV>
-__global__ void __launch_bounds__(NORM_THREADS) norm_kernel(const __grid_constant__ NormParams P) {
+// LAYER: rows are centred.  BIAS: some norm has a bias.
+template <typename TS, typename TB, int VEC, int NV, bool LAYER, bool BIAS>
+__global__ void __launch_bounds__(NORM_THREADS, NV == 1 && !BIAS ? 2 : 1) norm_kernel(const __grid_constant__ NormParams P) {
   extern __shared__ char slots[];
   __shared__ __align__(16) GroupBuf buf;
   clear(buf);
@@ -251,64 +281,88 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_kernel(const __grid_constan
   };
   for (int s = 0; s + 1 < P.slots; ++s) fetch(row0 + s * step, s);
   int slot = 0;
-  float A[NV][8], B[NV][8], wp[NV][8], bp[NV][8];  // b g w_post, b g b_post, w_pre, b_pre
-  if (P.y) {
-    load_param<VEC, NV>(P.w_post, P.pdt, 1.0f, tid, group, dim, A);
-    load_param<VEC, NV>(P.b_post, P.pdt, 0.0f, tid, group, dim, B);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = col_of<VEC>(tid, group, j, k);
-        const float g = P.gate_mode == DP_GATE_CHANNEL && c < dim ? P.b * param_at(P.gate, c, P.pdt, 1.0f) : P.b;
-        A[j][k] *= g;
-        B[j][k] *= g;
-      }
-  }
-  if (P.pre) {
-    load_param<VEC, NV>(P.w_pre, P.pdt, 1.0f, tid, group, dim, wp);
-    load_param<VEC, NV>(P.b_pre, P.pdt, 0.0f, tid, group, dim, bp);
-  }
-  for (int64_t row = row0; row < P.rows; row += step) {
-    fetch(row + (P.slots - 1) * step, slot == 0 ? P.slots - 1 : slot - 1);
-    if (VEC) fetch_wait(P.slots - 1);
-    const char* here = mine + slot * slot_bytes;
-    if (++slot == P.slots) slot = 0;
-    RowS xr;
-    xr.load(here + at_x, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
-    float r[NV][8];
-    if (P.y) {
-      RowB yr;
-      yr.load(here, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
-      float v[NV][8];
-#pragma unroll
-      for (int j = 0; j < NV; ++j) yr.w[j].unpack(v[j]);
-      float2 st = make_float2(0.0f, 1.0f);
-      if (P.post) {
-        st = row_stats<VEC, NV>(v, P.layer, P.eps, tid, group, dim, buf, half);
-        if (P.post_stats && tid == 0) P.post_stats[row] = st;
-      }
-      const float gt = P.gate_mode == DP_GATE_TOKEN ? param_at(P.gate, row, P.pdt, 1.0f) : 1.0f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        xr.w[j].unpack(r[j]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          r[j][k] = fmaf(P.a, r[j][k], gt * fmaf((v[j][k] - st.x) * st.y, A[j][k], B[j][k]));
-      }
-      store_row<TS, VEC, NV>(static_cast<TS*>(P.r) + row * dim, tid, group, dim, r);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) xr.w[j].unpack(r[j]);
-    }
-    if (P.pre) {
-      const float2 st = row_stats<VEC, NV>(r, P.layer, P.eps, tid, group, dim, buf, half);
-      if (P.pre_stats && tid == 0) P.pre_stats[row] = st;
+  const bool token = P.gate_mode == DP_GATE_TOKEN;
+  f2_t A[NV][4], B[NV][4], wp[NV][4], bp[NV][4];  // b g w_post, b g b_post, w_pre, b_pre
+  {
+    float g[NV][8], w[NV][8];
+    auto pairs = [&](f2_t (&to)[NV][4], bool scaled) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) r[j][k] = fmaf((r[j][k] - st.x) * st.y, wp[j][k], bp[j][k]);
-      store_row<TB, VEC, NV>(static_cast<TB*>(P.z) + row * dim, tid, group, dim, r);
+        for (int k = 0; k < 4; ++k)
+          to[j][k] = scaled ? f2_pack(w[j][2 * k] * g[j][2 * k], w[j][2 * k + 1] * g[j][2 * k + 1]) : f2_pack(w[j][2 * k], w[j][2 * k + 1]);
+    };
+    load_param<VEC, NV>(P.gate_mode == DP_GATE_CHANNEL ? P.gate : nullptr, P.pdt, 1.0f, tid, group, dim, g);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g[j][k] *= P.b;
+    load_param<VEC, NV>(P.w_post, P.pdt, 1.0f, tid, group, dim, w);
+    pairs(A, true);
+    load_param<VEC, NV>(P.w_pre, P.pdt, 1.0f, tid, group, dim, w);
+    pairs(wp, false);
+    if (BIAS) {
+      load_param<VEC, NV>(P.b_post, P.pdt, 0.0f, tid, group, dim, w);
+      pairs(B, true);
+      load_param<VEC, NV>(P.b_pre, P.pdt, 0.0f, tid, group, dim, w);
+      pairs(bp, false);
+    }
+  }
+  const float inv = 1.0f / (float)dim;
+  uint32_t next_gate = P.pdt == DP_BF16 ? 0x3f80u : 0x3f800000u;  // as it lies in memory: a conversion would wait for it
+  auto scalars = [&](int64_t row) {
+    if (token && row < P.rows)
+      next_gate = P.pdt == DP_BF16 ? __ldg(static_cast<const uint16_t*>(P.gate) + row) : __ldg(static_cast<const uint32_t*>(P.gate) + row);
+  };
+  scalars(row0);
+
+  for (int64_t row = row0; row < P.rows; row += step) {
+    fetch(row + (P.slots - 1) * step, slot == 0 ? P.slots - 1 : slot - 1);
+    const float gt = __uint_as_float(P.pdt == DP_BF16 ? next_gate << 16 : next_gate);
+    scalars(row + step);
+    if (VEC) fetch_wait(P.slots - 1);
+    const char* here = mine + slot * slot_bytes;
+    if (++slot == P.slots) slot = 0;
+    f2_t r[NV][4];
+    {
+      RowS xr;
+      xr.load(here + at_x, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) xr.w[j].unpack2(r[j]);
+    }
+    if (P.y) {
+      RowB yr;
+      yr.load(here, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+      f2_t v[NV][4];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) yr.w[j].unpack2(v[j]);
+      float2 st = make_float2(0.0f, 1.0f);
+      if (P.post) {
+        st = row_stats<VEC, NV, LAYER>(v, P.eps, inv, tid, group, dim, buf, half);
+        if (P.post_stats && tid == 0) P.post_stats[row] = st;
+      }
+      const f2_t a = f2_both(P.a), rstd = f2_both(st.y), gate = f2_both(gt);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const f2_t ax = f2_mul(a, r[j][k]), n = f2_mul(v[j][k], A[j][k]);
+          r[j][k] = f2_fma(BIAS ? f2_fma(n, rstd, B[j][k]) : f2_mul(n, rstd), gate, ax);
+        }
+      store_row2<TS, VEC, NV>(static_cast<TS*>(P.r) + row * dim, tid, group, dim, r);
+    }
+    if (P.pre) {
+      const float2 st = row_stats<VEC, NV, LAYER>(r, P.eps, inv, tid, group, dim, buf, half);
+      if (P.pre_stats && tid == 0) P.pre_stats[row] = st;
+      const f2_t rstd = f2_both(st.y);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const f2_t n = f2_mul(r[j][k], wp[j][k]);
+          r[j][k] = BIAS ? f2_fma(n, rstd, bp[j][k]) : f2_mul(n, rstd);
+        }
+      store_row2<TB, VEC, NV>(static_cast<TB*>(P.z) + row * dim, tid, group, dim, r);
     }
   }
 }
@@ -361,12 +415,13 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
     float v[NV][8];
     if (has_y) {
       load_param<VEC, NV>(P.w_post, P.pdt, 1.0f, tid, group, dim, v);
+      float g[NV][8];
+      load_param<VEC, NV>(P.gate_mode == DP_GATE_CHANNEL ? P.gate : nullptr, P.pdt, 1.0f, tid, group, dim, g);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int c = col_of<VEC>(tid, group, j, k);
-          v[j][k] *= P.gate_mode == DP_GATE_CHANNEL && c < dim ? P.b * param_at(P.gate, c, P.pdt, 1.0f) : P.b;
+          v[j][k] *= P.b * g[j][k];
           if (k & 1) A[j][k >> 1] = f2_pack(v[j][k - 1], v[j][k]);
         }
     }
@@ -635,9 +690,11 @@ int launch_rows(K kernel, Plan1& c, const Shape& s, NormParams& P, int64_t set, 
 
 template <typename TS, typename TB, int VEC, int NV>
 void run_forward(NormParams P, const Shape& s, cudaStream_t stream) {
-  static thread_local Plan1 plan;
-  launch_rows(norm_kernel<TS, TB, VEC, NV>, plan, s, P, VEC ? (int64_t)s.threads * NV * 8 * (sizeof(TS) + sizeof(TB)) : 0, 0,
-              INT32_MAX, stream);
+  static thread_local Plan1 plan[4];
+  const bool bias = P.b_post || P.b_pre;
+  auto k = P.layer ? (bias ? norm_kernel<TS, TB, VEC, NV, true, true> : norm_kernel<TS, TB, VEC, NV, true, false>)
+                   : (bias ? norm_kernel<TS, TB, VEC, NV, false, true> : norm_kernel<TS, TB, VEC, NV, false, false>);
+  launch_rows(k, plan[2 * P.layer + bias], s, P, VEC ? (int64_t)s.threads * NV * 8 * (sizeof(TS) + sizeof(TB)) : 0, 0, INT32_MAX, stream);
 }
 template <typename TS, typename TB, int VEC, int NV>
 int run_grad(NormParams P, const Shape& s, bool sum0, cudaStream_t stream) {

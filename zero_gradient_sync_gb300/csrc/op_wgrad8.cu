@@ -234,9 +234,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
+  grid_go();
   if (warp == 0) {
     // ---------------------------------------------------------------- two slabs of dy and two of x a step
     if (lane == 0) {
+      grid_wait();  // x has been decoded; nothing else here reads or writes memory before the first product is there
       int s = 0, phase = 0;
       bool ok = true;
       for (int32_t item = pair; ok && item < P.items; item += pairs) {
@@ -357,17 +359,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-// dw (+)= the slices' products in order, for the tiles that were split: one row of one tile a CTA.
+// dw (+)= the slices' products in order, for the tiles that were split: four rows of one tile a CTA, four columns a thread.
 __global__ void __launch_bounds__(BN) wgrad8_join_kernel(const __grid_constant__ WgradParams P) {
-  const int which = blockIdx.x / BM, r = blockIdx.x % BM;
+  grid_wait();
+  const int which = blockIdx.x / (BM / 4), r = blockIdx.x % (BM / 4) * 4 + threadIdx.x / 64, c = threadIdx.x % 64 * 4;
   const int tile = P.whole + which, tr = tile / P.tiles_k;
-  const int64_t row = (int64_t)tr * BM + r, col = (int64_t)(tile - tr * P.tiles_k) * BN + threadIdx.x;
+  const int64_t row = (int64_t)tr * BM + r, col = (int64_t)(tile - tr * P.tiles_k) * BN + c;
   if (row >= P.n || col >= P.k) return;
-  const float* part = P.part + ((int64_t)which * P.slices * BM + r) * BN + threadIdx.x;
-  float v = 0.0f;
+  const float4* part = reinterpret_cast<const float4*>(P.part + ((int64_t)which * P.slices * BM + r) * BN + c);
+  float v[4] = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int s = 0; s < P.slices; ++s) v += part[(int64_t)s * BM * BN];
-  grad_put(P.dw, row * P.k + col, P.dtype, P.accumulate, v);
+  for (int s = 0; s < P.slices; ++s) {
+    const float4 x = part[(int64_t)s * BM * BN / 4];
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + i < P.k) grad_put(P.dw, row * P.k + col + i, P.dtype, P.accumulate, v[i]);
 }
 
 // dy with rows that TMA cannot read, to rows of ld elements (a multiple of 8).
@@ -380,8 +388,8 @@ __global__ void __launch_bounds__(256) wgrad8_copy_kernel(uint16_t* dst, int64_t
 struct Split {
   int64_t tiles_k, tiles, whole, left, slices, all_steps, steps;
 };
-// Whole waves of tiles stay whole.  The rest is split into the number of slices that takes the least time, counted in steps:
-// waves x (steps of a slice + 4 for storing its product).
+// Whole waves of tiles stay whole.  The rest is split into the number of slices that takes the least time, counted in steps (of
+// 0.27 us): waves x (steps of a slice + 4 for storing its product), and 16 for the join.
 Split split_of(int64_t rows, int64_t n, int64_t k) {
   Split s;
   const int64_t pairs = sm_count() / 2;
@@ -393,7 +401,7 @@ Split split_of(int64_t rows, int64_t n, int64_t k) {
   s.slices = 1;
   int64_t best = s.all_steps + 4;
   for (int64_t c = 2; s.left > 0 && c <= MAX_SLICES && c * 4 <= s.all_steps; ++c) {
-    const int64_t cost = (s.left * c + pairs - 1) / pairs * ((s.all_steps + c - 1) / c + 4);
+    const int64_t cost = (s.left * c + pairs - 1) / pairs * ((s.all_steps + c - 1) / c + 4) + 16;
     if (cost < best) best = cost, s.slices = c;
   }
   s.steps = (s.all_steps + s.slices - 1) / s.slices;
@@ -490,8 +498,14 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
   CUtensorMap map_x, map_dy;
   DP_TRY(map_of(&map_x, base, pitch, rows, pitch));
   DP_TRY(map_of(&map_dy, aligned ? (const void*)dy : base + w.dy, n, rows, aligned ? lddy : w.lddy));
-  const cudaError_t attr = cudaFuncSetAttribute(wgrad8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (attr != cudaSuccess) return op_fail(DP_ERR_CUDA, "weight gradient: %s", cudaGetErrorString(attr));
+  static thread_local int ready = -1;  // the device whose kernel has its shared memory granted
+  int device = 0;
+  cudaGetDevice(&device);
+  if (ready != device) {
+    const cudaError_t attr = cudaFuncSetAttribute(wgrad8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (attr != cudaSuccess) return op_fail(DP_ERR_CUDA, "weight gradient: %s", cudaGetErrorString(attr));
+    ready = device;
+  }
   DP_TRY(dp_ckpt8_decode(base, codes, scales, rows, pitch, pitch, DP_BF16, stream_));
   int launches = 1;
   if (!aligned) {
@@ -516,11 +530,22 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
   P.accumulate = accumulate;
   P.timeout_ns = dp_get_wait_timeout_ns();
   const int64_t pairs = sm_count() / 2;
-  wgrad8_kernel<<<(unsigned)(2 * (P.items < pairs ? P.items : pairs)), THREADS, SMEM, stream>>>(P, map_dy, map_x);
-  if (s.slices > 1) {
-    wgrad8_join_kernel<<<(unsigned)(s.left * BM), BN, 0, stream>>>(P);
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(2 * (P.items < pairs ? P.items : pairs)));
+  c.blockDim = dim3(THREADS);
+  c.dynamicSmemBytes = SMEM;
+  c.stream = stream;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = a;
+  c.numAttrs = 1;
+  cudaError_t err = cudaLaunchKernelEx(&c, wgrad8_kernel, P, map_dy, map_x);
+  if (err == cudaSuccess && s.slices > 1) {
+    err = launch_after(wgrad8_join_kernel, s.left * (BM / 4), dim3(BN), stream, P);
     ++launches;
   }
+  if (err != cudaSuccess) return op_fail(DP_ERR_CUDA, "weight gradient launch: %s", cudaGetErrorString(err));
   return op_launched("weight gradient launch", launches);
 }
 

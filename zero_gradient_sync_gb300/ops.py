@@ -11,7 +11,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import LIB, DPError, _check, _stream, c_f32, c_i32, c_i64, c_vp, DP_ERR_INVALID_ARG
+from ._lib import LIB, DPError, _check, c_f32, c_i32, c_i64, c_vp, DP_ERR_INVALID_ARG
 
 DP_BF16, DP_F32 = 0, 1
 DP_NORM_RMS, DP_NORM_LAYER = 0, 1
@@ -57,6 +57,17 @@ _DTYPE = {torch.bfloat16: DP_BF16, torch.float32: DP_F32}
 _BF16, _U8, _I8, _F32 = torch.bfloat16, torch.uint8, torch.int8, torch.float32
 
 
+_raw_stream, _device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _stream(stream) -> int:
+    """cudaStream_t of the current stream (without building a Stream object where torch allows: 0.2 us instead of 2.8), or of
+    `stream`."""
+    if stream is None:
+        return _raw_stream(_device()) if _raw_stream and _device else torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _dtype(t, name: str) -> int:
     d = _DTYPE.get(t.dtype)
     if d is None:
@@ -64,18 +75,22 @@ def _dtype(t, name: str) -> int:
     return d
 
 
-def _arg(t, shape: Tuple[int, ...], dtype, name: str) -> int:
-    """Address of a contiguous CUDA tensor of this shape and type; None -> NULL."""
-    if t is None:
-        return 0
+def _refuse(t, shape, dtype, name: str):
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
         raise ValueError("%s: %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _arg(t, shape: Tuple[int, ...], dtype, name: str) -> int:
+    """Address of a contiguous CUDA tensor of this shape and type; None -> NULL."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, shape, dtype, name)
     return t.data_ptr()
 
 
@@ -83,12 +98,10 @@ def _rows(t, shape: Tuple[int, ...], dtype, name: str) -> Tuple[int, int]:
     """Address and row stride of a CUDA matrix whose rows are contiguous; None -> (NULL, 0)."""
     if t is None:
         return 0, 0
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype != dtype:
-        raise ValueError("%s: %s, expected %s" % (name, t.dtype, dtype))
-    if t.shape != shape:
-        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        _refuse(t, shape, dtype, name)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     rows, dim = shape
     if dim > 1 and t.stride(1) != 1:
         raise ValueError("%s: rows must be contiguous" % name)
@@ -155,7 +168,7 @@ def dp_embedding_grad(dtable, dout, ids, scale: float = 1.0, pad_id: int = -1, a
 # -------------------------------------------------------------------------------------------- norms around a block
 
 def _norm_params(x, y, z, params, kind, norms, gate, gate_per_token, res_scale, branch_scale, eps, accumulate):
-    rows, dim = _matrix(x, "x" if z is not None or y is not None else "r")
+    rows, dim = _matrix(x, "x")
     pdt = next((p.dtype for p in params if p is not None), _F32)
     block = y if y is not None else z
     bdt = block.dtype if block is not None else x.dtype
