@@ -61,3 +61,51 @@ def norm64(v, w, b, stats):
 def stats64(v, layer, eps):
     mean = v.mean(1, keepdim=True) if layer else torch.zeros(v.shape[0], 1, dtype=v.dtype, device=v.device)
     return torch.cat([mean, ((v - mean) ** 2).mean(1, keepdim=True).add(eps).rsqrt()], 1)
+
+
+def gate64(s, gate):
+    if s["gate"] is None:
+        return 1.0
+    return s["gate"].double() if gate == "channel" else s["gate"].double()[:, None]
+
+
+def norm_grad64(s, gate, layer, a, b, ps, qs, post=True, pre=True):
+    """The gradient's formulas in 64 bits, with the magnitudes that its sums run over."""
+    dim = s["r"].shape[1] if s.get("r") is not None else s["y"].shape[1]
+    out, mag = {}, {}
+    D = torch.zeros(s["dx_shape"], dtype=torch.float64, device=s["w_pre"].device) if s["dr"] is None else s["dr"].double()
+    eD = D.abs() * 2
+    if pre:
+        rh = (s["r"].double() - qs[:, :1]) * qs[:, 1:]
+        rm = (s["r"].double().abs() + qs[:, :1].abs()) * qs[:, 1:]
+        dz = s["dz"].double()
+        v = dz * s["w_pre"].double()
+        c1 = (v * rh).mean(1, keepdim=True)
+        c0 = v.mean(1, keepdim=True) if layer else 0.0
+        D = D + qs[:, 1:] * (v - rh * c1 - c0)
+        m1 = (v.abs() * rm).mean(1, keepdim=True)
+        m0 = v.abs().mean(1, keepdim=True)
+        eD = eD + qs[:, 1:] * (v.abs() + rm * m1 * 2 + m0)
+        out["dw_pre"], out["db_pre"] = (dz * rh).sum(0), dz.sum(0)
+        mag["dw_pre"], mag["db_pre"] = (dz.abs() * rm).sum(0), dz.abs().sum(0)
+    out["dx"], mag["dx"] = a * D, eD * a
+    if s["y"] is not None:
+        y = s["y"].double()
+        yh = (y - ps[:, :1]) * ps[:, 1:] if post else y
+        ym = (y.abs() + ps[:, :1].abs()) * ps[:, 1:] if post else y.abs()
+        w = s["w_post"].double() if post else torch.ones(dim, dtype=torch.float64, device=s["w_pre"].device)
+        c = s["b_post"].double() if post and s["b_post"] is not None else torch.zeros_like(w)
+        g = gate64(s, gate)
+        ga = torch.as_tensor(g).abs()
+        v = b * g * w * D
+        ev = b * ga * w.abs() * eD
+        if post:
+            out["dy"] = ps[:, 1:] * (v - yh * (v * yh).mean(1, keepdim=True) - (v.mean(1, keepdim=True) if layer else 0.0))
+            mag["dy"] = ps[:, 1:] * (ev + 2 * ym * (ev * ym).mean(1, keepdim=True) + ev.mean(1, keepdim=True))
+        else:
+            out["dy"], mag["dy"] = v, ev
+        out["dw_post"], mag["dw_post"] = (b * g * D * yh).sum(0), (b * ga * eD * ym).sum(0)
+        out["db_post"], mag["db_post"] = (b * g * D).sum(0) * torch.ones_like(w), (b * ga * eD).sum(0) * torch.ones_like(w)
+        axis = 0 if gate == "channel" else 1
+        out["dgate"], mag["dgate"] = (b * D * (yh * w + c)).sum(axis), (b * eD * (ym * w.abs() + c.abs())).sum(axis)
+    return out, mag

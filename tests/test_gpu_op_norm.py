@@ -30,12 +30,6 @@ def build(rows, dim, layer, gate, ts, tb, tp, off, seed=0, mean=0.3):
     return s, mk, checks
 
 
-def g64(s, gate):
-    if s["gate"] is None:
-        return 1.0
-    return s["gate"].double() if gate == "channel" else s["gate"].double()[:, None]
-
-
 def d64(t):
     return None if t is None else t.double()
 
@@ -61,11 +55,11 @@ def test_forward(dev, kind, gate, rows, dim, off):
         y, x = s["y"].double(), s["x"].double()
         ps = ou.stats64(y, layer, 2.0 ** -16)
         h, n = ou.norm64(y, d64(s["w_post"]), d64(s["b_post"]), ps)
-        want = a * x + b * g64(s, gate) * n
+        want = a * x + b * ou.gate64(s, gate) * n
         # errors of the mean (against the row's mean magnitude) and of rstd (relative) reach every element
         spread = y.abs().mean(1, keepdim=True) * ps[:, 1:] + h.abs()
         en = K * ou.EPS * (spread * s["w_post"].double().abs() + n.abs())
-        er = en * b * torch.as_tensor(g64(s, gate)).abs() + 4 * ou.EPS * (a * x.abs() + want.abs())
+        er = en * b * torch.as_tensor(ou.gate64(s, gate)).abs() + 4 * ou.EPS * (a * x.abs() + want.abs())
         ou.close(r, want, er, "r")
         sx = K * ou.EPS * (y.abs().mean(1) + 1e-30)
         ou.close(post[:, 0].contiguous(), ps[:, 0], sx, "post mean")
@@ -80,48 +74,6 @@ def test_forward(dev, kind, gate, rows, dim, off):
         ou.close(z, nz, ez, "z")
         for c in checks:
             c()
-
-
-def grad64(s, gate, layer, a, b, ps, qs, post=True, pre=True):
-    """The gradient's formulas in 64 bits, with the magnitudes that its sums run over."""
-    dim = s["r"].shape[1] if s.get("r") is not None else s["y"].shape[1]
-    out, mag = {}, {}
-    D = torch.zeros(s["dx_shape"], dtype=torch.float64, device="cuda") if s["dr"] is None else s["dr"].double()
-    eD = D.abs() * 2
-    if pre:
-        rh = (s["r"].double() - qs[:, :1]) * qs[:, 1:]
-        rm = (s["r"].double().abs() + qs[:, :1].abs()) * qs[:, 1:]
-        dz = s["dz"].double()
-        v = dz * s["w_pre"].double()
-        c1 = (v * rh).mean(1, keepdim=True)
-        c0 = v.mean(1, keepdim=True) if layer else 0.0
-        D = D + qs[:, 1:] * (v - rh * c1 - c0)
-        m1 = (v.abs() * rm).mean(1, keepdim=True)
-        m0 = v.abs().mean(1, keepdim=True)
-        eD = eD + qs[:, 1:] * (v.abs() + rm * m1 * 2 + m0)
-        out["dw_pre"], out["db_pre"] = (dz * rh).sum(0), dz.sum(0)
-        mag["dw_pre"], mag["db_pre"] = (dz.abs() * rm).sum(0), dz.abs().sum(0)
-    out["dx"], mag["dx"] = a * D, eD * a
-    if s["y"] is not None:
-        y = s["y"].double()
-        yh = (y - ps[:, :1]) * ps[:, 1:] if post else y
-        ym = (y.abs() + ps[:, :1].abs()) * ps[:, 1:] if post else y.abs()
-        w = s["w_post"].double() if post else torch.ones(dim, dtype=torch.float64, device="cuda")
-        c = s["b_post"].double() if post and s["b_post"] is not None else torch.zeros_like(w)
-        g = g64(s, gate)
-        ga = torch.as_tensor(g).abs()
-        v = b * g * w * D
-        ev = b * ga * w.abs() * eD
-        if post:
-            out["dy"] = ps[:, 1:] * (v - yh * (v * yh).mean(1, keepdim=True) - (v.mean(1, keepdim=True) if layer else 0.0))
-            mag["dy"] = ps[:, 1:] * (ev + 2 * ym * (ev * ym).mean(1, keepdim=True) + ev.mean(1, keepdim=True))
-        else:
-            out["dy"], mag["dy"] = v, ev
-        out["dw_post"], mag["dw_post"] = (b * g * D * yh).sum(0), (b * ga * eD * ym).sum(0)
-        out["db_post"], mag["db_post"] = (b * g * D).sum(0) * torch.ones_like(w), (b * ga * eD).sum(0) * torch.ones_like(w)
-        axis = 0 if gate == "channel" else 1
-        out["dgate"], mag["dgate"] = (b * D * (yh * w + c)).sum(axis), (b * eD * (ym * w.abs() + c.abs())).sum(axis)
-    return out, mag
 
 
 @pytest.mark.parametrize("kind", ["rms", "layer"])
@@ -143,7 +95,7 @@ def test_gradient(dev, kind, gate, rows, dim, off):
                               gate_per_token=gate == "token", w_pre=s["w_pre"],
                               kind=dp.DP_NORM_LAYER if layer else dp.DP_NORM_RMS, res_scale=a, branch_scale=b,
                               post_stats=ps32, pre_stats=qs32, accumulate=accumulate, ws=ws, **grads)
-        want, mag = grad64(s, gate, layer, a, b, ps32.double(), qs32.double())
+        want, mag = ou.norm_grad64(s, gate, layer, a, b, ps32.double(), qs32.double())
         ou.close(dx, want["dx"], K * ou.EPS * mag["dx"], "dx")
         ou.close(dy, want["dy"], K * ou.EPS * mag["dy"], "dy")
         for k in names:
@@ -170,7 +122,7 @@ def test_parts_left_out(dev, kind):
     ou.close(r, s["x"].double() + s["gate"].double() * s["y"].double(), 4 * ou.EPS * (s["x"].double().abs() + (s["gate"].double() * s["y"].double()).abs()), "r")
     dx, dy, dgate = mk((rows, dim), BF), mk((rows, dim), BF), mk((dim,), BF)
     dp.dp_block_norm_grad(dx, dy, s["dr"], None, s["r"], s["y"], gate=s["gate"], post=False, pre=False, kind=code, dgate=dgate, ws=ws)
-    want, mag = grad64(s, "channel", layer, 1.0, 1.0, None, None, post=False, pre=False)
+    want, mag = ou.norm_grad64(s, "channel", layer, 1.0, 1.0, None, None, post=False, pre=False)
     for k, t in (("dx", dx), ("dy", dy), ("dgate", dgate)):
         ou.close(t, want[k], (rows + K) * ou.EPS * mag[k], k)
     # only the norm before the first block: z = N(x); r is x
@@ -180,7 +132,7 @@ def test_parts_left_out(dev, kind):
     h, n = ou.norm64(s["x"].double(), d64(s["w_pre"]), d64(s["b_pre"]), xs)
     ou.close(z, n, K * ou.EPS * (1 + h.abs()) * 2 * s["w_pre"].double().abs() + K * ou.EPS * n.abs(), "z")
     q = dict(s, y=None, dr=None)
-    want, mag = grad64(q, "none", layer, 1.0, 1.0, None, qs.double())
+    want, mag = ou.norm_grad64(q, "none", layer, 1.0, 1.0, None, qs.double())
     dw = mk((dim,), BF)
     dp.dp_block_norm_grad(dx, None, None, s["dz"], s["r"], w_pre=s["w_pre"], kind=code, pre_stats=qs, dw_pre=dw, ws=ws)
     ou.close(dx, want["dx"], K * ou.EPS * mag["dx"], "dx")
