@@ -159,7 +159,7 @@ __device__ __forceinline__ Kept get_ckpt(const Ckpt& c, const Place& p, int pitc
   return k;
 }
 
-constexpr int COPY_U = 4, ACT_U = 2;  // pieces of a thread
+constexpr int COPY_U = 4, ACT_U = 3;  // pieces of a thread (8k x 11008: 1 137 + 146, 2 121 + 152, 3 121 + 149, 4 125 + 160 us)
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS) encode_kernel(Ckpt c, const T* x, int64_t ldx, Walk W, int vec) {
@@ -191,30 +191,51 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(T* x, int64_t ldx, Ckpt
   }
 }
 
-// f(g) and f'(g), with s the logistic function.  SiLU: f = g s(g), f' = s (1 + g (1 - s)).  GELU's tanh form is
+// f(g) and f'(g) of a pair, with s the logistic function.  SiLU: f = g s(g), f' = s (1 + g (1 - s)).  GELU's tanh form is
 // f = g s(2y), y = c (g + 0.044715 g^3), c = sqrt(2 / pi), since (1 + tanh y) / 2 = s(2y); f' = s + 2 f (1 - s) c (1 +
-// 0.134145 g^2).  With t = e^-|v| and q = 1 / (1 + t), s(v) and 1 - s(v) are q and t q, or the reverse: neither cancels,
-// and t runs out of range only where it is below fp32.  g^2 stops at 10^4, where t has long been 0, so that no product of
-// infinity and zero appears.
-__device__ __forceinline__ void logistic(float v, float& s, float& rest) {
-  const float t = __expf(-fabsf(v));
-  const float q = __fdividef(1.0f, 1.0f + t), tq = t * q;
-  s = v < 0.0f ? tq : q;
-  rest = v < 0.0f ? q : tq;
+// 0.134145 g^2).  With t = e^-|v| and q = 1 / (1 + t), s(v) and 1 - s(v) are q and t q, or the reverse: neither cancels.
+// t is taken as 2^-24 2^(24 - |v| log2 e), so that the hardware's power of two, which makes zeros of subnormal results, loses
+// none.  g^2 stops at 10^4, where t has long been 0, so that no product of infinity and zero appears.  The short activation
+// kernels are bound by instructions (1001 x 8192 in fp32 one by one: 16.4 us), hence pairs and single-instruction functions.
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void logistic(f2_t v, f2_t& s, f2_t& rest) {
+  float a, b, ta, tb, qa, qb;
+  f2_unpack(v, a, b);
+  f2_t x = f2_fma(f2_pack(fabsf(a), fabsf(b)), f2_both(-1.4426950408889634f), f2_both(24.0f));
+  f2_unpack(x, ta, tb);
+  const f2_t t = f2_mul(f2_pack(exp2_ftz(ta), exp2_ftz(tb)), f2_both(5.9604644775390625e-8f));
+  x = f2_add(t, f2_both(1.0f));
+  f2_unpack(x, qa, qb);
+  qa = rcp_ftz(qa);
+  qb = rcp_ftz(qb);
+  f2_unpack(f2_mul(t, f2_pack(qa, qb)), ta, tb);
+  s = f2_pack(a < 0.0f ? ta : qa, b < 0.0f ? tb : qb);
+  rest = f2_pack(a < 0.0f ? qa : ta, b < 0.0f ? qb : tb);
 }
 template <int ACT>
-__device__ __forceinline__ void act_of(float g, float& f, float& df) {
-  float s, rest;
+__device__ __forceinline__ void act_of(f2_t g, f2_t& f, f2_t& df) {
+  f2_t s, rest;
   if (ACT == DP_ACT_SILU) {
     logistic(g, s, rest);
-    f = g * s;
-    df = s * fmaf(g, rest, 1.0f);
+    f = f2_mul(g, s);
+    df = f2_mul(s, f2_fma(g, rest, f2_both(1.0f)));
   } else {
-    const float c = 0.7978845608028654f;
-    const float g2 = fminf(g * g, 1e4f);
-    logistic(2.0f * c * g * fmaf(0.044715f, g2, 1.0f), s, rest);
-    f = g * s;
-    df = fmaf(f * rest, 2.0f * c * fmaf(0.134145f, g2, 1.0f), s);
+    const float c2 = 2.0f * 0.7978845608028654f;
+    float a, b;
+    f2_unpack(f2_mul(g, g), a, b);
+    const f2_t g2 = f2_pack(fminf(a, 1e4f), fminf(b, 1e4f));
+    logistic(f2_mul(g, f2_fma(g2, f2_both(c2 * 0.044715f), f2_both(c2))), s, rest);
+    f = f2_mul(g, s);
+    df = f2_fma(f2_mul(f, rest), f2_fma(g2, f2_both(c2 * 0.134145f), f2_both(c2)), s);
   }
 }
 
@@ -240,11 +261,9 @@ __global__ void __launch_bounds__(THREADS) act_kernel(bf16_t* h, const bf16_t* g
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float a, b, fa, fb, unused;
-      f2_unpack(gv[k], a, b);
-      act_of<ACT>(a, fa, unused);
-      act_of<ACT>(b, fb, unused);
-      gv[k] = GATED ? f2_mul(f2_pack(fa, fb), uv[k]) : f2_pack(fa, fb);
+      f2_t f, unused;
+      act_of<ACT>(gv[k], f, unused);
+      gv[k] = GATED ? f2_mul(f, uv[k]) : f;
     }
     store_piece(h, ldh, p[i], W.dim, vec, gv);
   }
@@ -271,11 +290,8 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(bf16_t* dg, bf16_t* d
     if (GATED) values_of(uk[i].codes, uk[i].E, uv);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float a, b, fa, fb, da, db;
-      f2_unpack(gv[k], a, b);
-      act_of<ACT>(a, fa, da);
-      act_of<ACT>(b, fb, db);
-      const f2_t f = f2_pack(fa, fb), df = f2_pack(da, db);
+      f2_t f, df;
+      act_of<ACT>(gv[k], f, df);
       hv[k] = GATED ? f2_mul(f, uv[k]) : f;
       gv[k] = f2_mul(GATED ? f2_mul(dv[k], uv[k]) : dv[k], df);
       dv[k] = f2_mul(dv[k], f);

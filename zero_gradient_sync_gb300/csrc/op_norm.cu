@@ -596,16 +596,17 @@ struct FinishParams {
   float b;
 };
 
-// Adds the partial rows of 16 columns in 64 interleaved parts, then the parts in order.
+// Adds the partial rows of 16 columns: 64 threads a column take the parts in turn, then a warp adds the 64 in a fixed order.
 __global__ void __launch_bounds__(FIN_COLS* FIN_ROWS) norm_finish_kernel(const __grid_constant__ FinishParams P) {
-  __shared__ float sums[FIN_ROWS][4][FIN_COLS];
+  __shared__ float sums[4 * FIN_COLS][FIN_ROWS + 1];
+  __shared__ float done[4 * FIN_COLS];
   grid_wait();
-  const int c = blockIdx.x * FIN_COLS + threadIdx.x;
+  const int c0 = blockIdx.x * FIN_COLS + threadIdx.x;
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < P.dim) {
+  if (c0 < P.dim) {
 #pragma unroll 5
     for (int64_t i = threadIdx.y; i < P.parts; i += FIN_ROWS) {
-      const float* p = P.part + i * (P.sum0 ? 4 : 2) * P.dim + c;
+      const float* p = P.part + i * (P.sum0 ? 4 : 2) * P.dim + c0;
       s[0] += p[0];
       s[1] += p[P.dim];
       if (P.sum0) {
@@ -615,12 +616,20 @@ __global__ void __launch_bounds__(FIN_COLS* FIN_ROWS) norm_finish_kernel(const _
     }
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) sums[threadIdx.y][q][threadIdx.x] = s[q];
+  for (int q = 0; q < 4; ++q) sums[q * FIN_COLS + threadIdx.x][threadIdx.y] = s[q];
   __syncthreads();
-  if (threadIdx.y != 0 || c >= P.dim) return;
-  for (int y = 1; y < FIN_ROWS; ++y)
+  const int t = threadIdx.y * FIN_COLS + threadIdx.x, lane = t & 31;
+  for (int i = t >> 5; i < 4 * FIN_COLS; i += FIN_COLS * FIN_ROWS / 32) {
+    float v = sums[i][lane] + sums[i][lane + 32];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) s[q] += sums[y][q][threadIdx.x];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) done[i] = v;
+  }
+  __syncthreads();
+  const int c = blockIdx.x * FIN_COLS + t;
+  if (t >= FIN_COLS || c >= P.dim) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) s[q] = done[q * FIN_COLS + t];
   const float g = P.b * (P.gate_mode == DP_GATE_CHANNEL ? param_at(P.gate, c, P.pdt, 1.0f) : 1.0f);
   if (P.dw_post) grad_put(P.dw_post, c, P.pdt, P.accumulate, g * s[0]);
   if (P.db_post) grad_put(P.db_post, c, P.pdt, P.accumulate, g * s[2]);
