@@ -103,37 +103,26 @@ __device__ __forceinline__ void places_of(const Walk& W, Place (&p)[U]) {
 }
 
 // Pieces that are not there, or lie beyond the row's end, are zeros.  vec: dim is a multiple of 8 and rows 16-byte aligned.
+__device__ __forceinline__ int there(const Place& p, int dim) { return p.on ? there8(p.col, dim) : 0; }
 template <typename T>
-__device__ __forceinline__ Raw8<T> load_piece(const T* base, int64_t ld, const Place& p, int dim, int vec) {
+__device__ __forceinline__ Raw8<T> load_piece(const T* base, int64_t ld, const Place& p, const Walk& W, int vec) {
   const T* q = base + p.row * ld + p.col;
-  if (p.on && vec && p.col < dim) return load_raw8(q);
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (p.on && !vec) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (p.col + k < dim) v[k] = Elem<T>::get(q[k]);
+  if (vec) {
+    if (p.on && p.col < W.dim) return load_raw8(q);
+    const float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    Raw8<T> w;
+    w.pack(v);
+    return w;
   }
-  Raw8<T> w;
-  w.pack(v);
-  return w;
+  return load_any8(q, there(p, W.dim), base, base + (W.rows - 1) * ld + W.dim);
 }
 template <typename T>
-__device__ __forceinline__ void store_piece(T* base, int64_t ld, const Place& p, int dim, int vec, const f2_t (&v)[4]) {
+__device__ __forceinline__ void store_piece(T* base, int64_t ld, const Place& p, const Walk& W, int vec, const f2_t (&v)[4]) {
   T* q = base + p.row * ld + p.col;
-  if (!p.on) return;
-  if (vec) {
-    if (p.col >= dim) return;
-    Raw8<T> o;
-    o.pack2(v);
-    store_raw8(q, o);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float x[2];
-      f2_unpack(v[k >> 1], x[0], x[1]);
-      if (p.col + k < dim) q[k] = Elem<T>::put(x[k & 1]);
-    }
-  }
+  Raw8<T> o;
+  o.pack2(v);
+  if (!vec) store_any8(q, there(p, W.dim), o);
+  else if (p.on && p.col < W.dim) store_raw8(q, o);
 }
 struct Ckpt {
   int8_t* codes;
@@ -167,7 +156,7 @@ __global__ void __launch_bounds__(THREADS) encode_kernel(Ckpt c, const T* x, int
   Raw8<T> w[COPY_U];
   places_of(W, p);
 #pragma unroll
-  for (int i = 0; i < COPY_U; ++i) w[i] = load_piece(x, ldx, p[i], W.dim, vec);
+  for (int i = 0; i < COPY_U; ++i) w[i] = load_piece(x, ldx, p[i], W, vec);
 #pragma unroll
   for (int i = 0; i < COPY_U; ++i) {
     f2_t v[4];
@@ -187,7 +176,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(T* x, int64_t ldx, Ckpt
   for (int i = 0; i < COPY_U; ++i) {
     f2_t v[4];
     values_of(k[i].codes, k[i].E, v);
-    store_piece(x, ldx, p[i], W.dim, vec, v);
+    store_piece(x, ldx, p[i], W, vec, v);
   }
 }
 
@@ -247,8 +236,8 @@ __global__ void __launch_bounds__(THREADS) act_kernel(bf16_t* h, const bf16_t* g
   places_of(W, p);
 #pragma unroll
   for (int i = 0; i < ACT_U; ++i) {
-    gw[i] = load_piece(g, ld, p[i], W.dim, vec);
-    if (GATED) uw[i] = load_piece(u, ld, p[i], W.dim, vec);
+    gw[i] = load_piece(g, ld, p[i], W, vec);
+    if (GATED) uw[i] = load_piece(u, ld, p[i], W, vec);
   }
 #pragma unroll
   for (int i = 0; i < ACT_U; ++i) {
@@ -265,7 +254,7 @@ __global__ void __launch_bounds__(THREADS) act_kernel(bf16_t* h, const bf16_t* g
       act_of<ACT>(gv[k], f, unused);
       gv[k] = GATED ? f2_mul(f, uv[k]) : f;
     }
-    store_piece(h, ldh, p[i], W.dim, vec, gv);
+    store_piece(h, ldh, p[i], W, vec, gv);
   }
 }
 
@@ -278,7 +267,7 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(bf16_t* dg, bf16_t* d
   places_of(W, p);
 #pragma unroll
   for (int i = 0; i < ACT_U; ++i) {
-    dw[i] = load_piece(dh, ldh, p[i], W.dim, vec);
+    dw[i] = load_piece(dh, ldh, p[i], W, vec);
     gk[i] = get_ckpt(g8, p[i], W.pieces * 8);
     if (GATED) uk[i] = get_ckpt(u8, p[i], W.pieces * 8);
   }
@@ -296,9 +285,9 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(bf16_t* dg, bf16_t* d
       gv[k] = f2_mul(GATED ? f2_mul(dv[k], uv[k]) : dv[k], df);
       dv[k] = f2_mul(dv[k], f);
     }
-    store_piece(dg, ld, p[i], W.dim, vec, gv);
-    if (GATED) store_piece(du, ld, p[i], W.dim, vec, dv);
-    if (h) store_piece(h, ldh, p[i], W.dim, vec, hv);
+    store_piece(dg, ld, p[i], W, vec, gv);
+    if (GATED) store_piece(du, ld, p[i], W, vec, dv);
+    if (h) store_piece(h, ldh, p[i], W, vec, hv);
   }
 }
 

@@ -116,6 +116,111 @@ __device__ __forceinline__ void store_raw8(float* p, const Raw8<float>& r) {
   }
 }
 
+// How many of the eight elements from c on a row of dim has.
+__device__ __forceinline__ int there8(int64_t c, int64_t dim) { return dim - c < 0 ? 0 : dim - c > 8 ? 8 : (int)(dim - c); }
+
+// ---- eight elements at any address
+//
+// Rows that are not 16-byte aligned (an odd width, a slice at an odd offset) would otherwise go element by element: eight
+// instructions for eight elements, each over every sector of the warp's piece, a quarter of the aligned path's rate.
+
+// Words i + by/4 .. of w, moved down by `by` bytes in all (0 <= by <= 16, a multiple of two).
+template <int N, int OUT>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[N], uint32_t by, uint32_t (&out)[OUT]) {
+  if (by & 16) {
+#pragma unroll
+    for (int i = 0; i + 4 < N; ++i) w[i] = w[i + 4];
+  }
+  if (by & 8) {
+#pragma unroll
+    for (int i = 0; i + 2 < N; ++i) w[i] = w[i + 2];
+  }
+  if (by & 4) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) w[i] = w[i + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i], i + 1 < N ? w[i + 1] : 0u, (by & 2) * 8);
+}
+
+// The first n (0..8) elements at p, zeros behind them.  Whole 16-byte words are read where they lie inside [lo, hi), the
+// tensor; the others' elements one by one.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_any8(const T* p, int n, const T* lo, const T* hi) {
+  constexpr int WORDS = sizeof(T) * 2;  // 32-bit words of eight elements
+  uint32_t out[WORDS];
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) out[i] = 0;
+  const uint32_t s = (uint32_t)(uintptr_t)p & 15u;
+  const char* first = reinterpret_cast<const char*>(p) - s;
+  const uint32_t need = s + (uint32_t)n * sizeof(T);  // bytes from `first`
+  const uint32_t whole = (need + 15u) & ~15u;
+  if (n > 0 && first >= reinterpret_cast<const char*>(lo) && first + whole <= reinterpret_cast<const char*>(hi)) {
+    uint32_t w[WORDS + 4];
+#pragma unroll
+    for (int q = 0; q <= WORDS / 4; ++q) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (need > 16u * q) x = *(reinterpret_cast<const uint4*>(first) + q);  // L1 has it for the next lane
+      w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
+    }
+    shift_words(w, s, out);
+    if (n < 8) {
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) {
+        const int left = n * (int)sizeof(T) - 4 * i;  // bytes of this word that count
+        out[i] &= left >= 4 ? 0xffffffffu : left == 2 ? 0xffffu : 0u;
+      }
+    }
+  } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 2 * WORDS; ++i)
+      if (i * 2 < n * (int)sizeof(T)) out[i >> 1] |= (uint32_t)h[i] << (16 * (i & 1));
+  }
+  Raw8<T> r;
+  uint32_t* to = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) to[i] = out[i];
+  return r;
+}
+
+// Writes the first n (0..8) elements of r to p; called by whole warps.  Where the next lane's elements follow this lane's in
+// memory, the 16-byte word that the two share is put together and written by the next lane; what no whole word covers is
+// written in halves of a word.
+template <typename T>
+__device__ __forceinline__ void store_any8(T* p, int n, const Raw8<T>& r) {
+  constexpr int WORDS = sizeof(T) * 2;
+  constexpr bool TWO = WORDS == 8;
+  const int lane = threadIdx.x & 31, bytes = n * (int)sizeof(T);
+  const uint32_t at = (uint32_t)(uintptr_t)p;
+  const int s = (int)(at & 15u), cut = 16 - s;  // aligned words begin at bytes -s, cut, cut + 16 of this lane's
+  uint32_t w[4 + WORDS], out[WORDS];
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) w[4 + i] = from[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, from[WORDS - 4 + i], 1);  // the previous lane's last 16 bytes
+  const uint32_t next_at = __shfl_down_sync(0xffffffffu, at, 1);
+  const int next_bytes = __shfl_down_sync(0xffffffffu, bytes, 1);
+  const bool gives = lane < 31 && n == 8 && next_at == at + 4 * WORDS && next_bytes >= cut;  // its bytes behind the last whole word
+  const bool takes = __shfl_up_sync(0xffffffffu, (int)gives, 1) != 0 && lane > 0;
+  shift_words(w, (uint32_t)cut, out);
+  char* first = reinterpret_cast<char*>(p) - s;
+  const bool word0 = (s == 0 || takes) && bytes >= cut, word1 = TWO && bytes >= cut + 16;
+  if (word0) *reinterpret_cast<uint4*>(first) = make_uint4(out[0], out[1], out[2], out[3]);
+  if (word1) *reinterpret_cast<uint4*>(first + 16) = make_uint4(out[WORDS - 4], out[WORDS - 3], out[WORDS - 2], out[WORDS - 1]);
+  const int tail = TWO ? cut + 16 : cut;
+  if (bytes > 0 && (!word0 || (TWO && !word1) || (bytes > tail && !gives))) {
+    uint16_t* h = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 2 * WORDS; ++i) {
+      const int b = 2 * i;
+      const bool written = b < cut ? word0 : b < tail ? word1 : gives;
+      if (b < bytes && !written) h[i] = (uint16_t)(from[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
 // A parameter of either type, at any element offset; NULL stands for `none`.
 __device__ __forceinline__ float param_at(const void* p, int64_t i, int dtype, float none) {
   if (!p) return none;

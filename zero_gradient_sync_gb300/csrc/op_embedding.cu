@@ -90,8 +90,16 @@ __global__ void __launch_bounds__(256) emb_lookup_kernel(T* __restrict__ out, co
         store_raw8(dst + c, o);
       }
     } else {
-#pragma unroll 4
-      for (int64_t c = lane; c < dim; c += 32) dst[c] = Elem<T>::put(live ? Elem<T>::get(src[c]) * scale : 0.0f);
+      for (int64_t c = lane * 8; c < dim + lane * 8; c += 256) {  // all lanes go round equally often
+        const int n = there8(c, dim);
+        Raw8<T> o = load_any8(src + c, live ? n : 0, table, table + vocab * dim);
+        float v[8];
+        o.unpack(v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= scale;
+        o.pack(v);
+        store_any8(dst + c, n, o);
+      }
     }
   }
 }
@@ -326,22 +334,16 @@ struct SumParams {
   int accumulate, chunk, slabs;
 };
 
+// Eight columns a lane of a row of a matrix of `rows` rows.
 template <typename T, int VEC>
-__device__ __forceinline__ Raw8<T> load_cols(const T* row, int64_t col0, int lane, int64_t dim) {
+__device__ __forceinline__ Raw8<T> load_cols(const T* base, int64_t row, int64_t rows, int64_t col0, int lane, int64_t dim) {
+  const int64_t c = col0 + lane * 8;
+  const T* p = base + row * dim + c;
+  if (!VEC) return load_any8(p, there8(c, dim), base, base + rows * dim);
+  if (c < dim) return load_raw8(p);
+  const float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   Raw8<T> w;
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (VEC) {
-    const int64_t c = col0 + lane * 8;
-    if (c < dim) w = load_raw8(row + c);
-    else w.pack(v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int64_t c = col0 + lane + 32 * k;
-      if (c < dim) v[k] = Elem<T>::get(row[c]);
-    }
-    w.pack(v);
-  }
+  w.pack(v);
   return w;
 }
 
@@ -359,20 +361,11 @@ __device__ __forceinline__ void finish_row(const SumParams& P, uint32_t key, int
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = __fadd_rn(o[k], v[k]);
   }
-  if (VEC) {
-    const int64_t c = col0 + lane * 8;
-    if (c < P.dim) {
-      Raw8<T> o;
-      o.pack(v);
-      store_raw8(row + c, o);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int64_t c = col0 + lane + 32 * k;
-      if (c < P.dim) row[c] = Elem<T>::put(v[k]);
-    }
-  }
+  const int64_t c = col0 + lane * 8;
+  Raw8<T> o;
+  o.pack(v);
+  if (!VEC) store_any8(row + c, there8(c, P.dim), o);
+  else if (c < P.dim) store_raw8(row + c, o);
 }
 
 // Partial rows are kept in the lanes' order (each lane's eight sums together): only the same lane reads them.
@@ -422,9 +415,9 @@ __global__ void __launch_bounds__(128) emb_sum_kernel(const __grid_constant__ Su
       const int j = min(j0 + u, live - 1);
       const uint32_t t = __shfl_sync(0xffffffffu, mytok, j), key = __shfl_sync(0xffffffffu, mykey, j);
       if (j0 + u < live) {
-        v[u] = load_cols<T, VEC>(static_cast<const T*>(P.dout) + (int64_t)t * P.dim, col0, lane, P.dim);
+        v[u] = load_cols<T, VEC>(static_cast<const T*>(P.dout), t, P.tokens, col0, lane, P.dim);
         if (ADD && (starts >> j & 1))
-          old[u] = load_cols<T, VEC>(static_cast<const T*>(P.dtable) + (int64_t)key * P.dim, col0, lane, P.dim);
+          old[u] = load_cols<T, VEC>(static_cast<const T*>(P.dtable), key, P.vocab, col0, lane, P.dim);
       }
     }
 #pragma unroll
@@ -489,7 +482,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) emb_join_kernel(const __grid_
       const int64_t chunk = P.list[1 + 2 * e];
       const uint32_t key = P.list[2 + 2 * e];
       Raw8<T> old = {};
-      if (P.accumulate) old = load_cols<T, VEC>(static_cast<const T*>(P.dtable) + (int64_t)key * P.dim, col0, lane, P.dim);
+      if (P.accumulate) old = load_cols<T, VEC>(static_cast<const T*>(P.dtable), key, P.vocab, col0, lane, P.dim);
       float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       add_part(part_at(P, chunk, 1, slab, lane), acc);
       // The run's last chunk is the last whose first key is the run's: looked for among the next 31, then 32 probes at a
@@ -531,7 +524,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) emb_join_kernel(const __grid_
       float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       Raw8<T> old = {};
       if (warp == 0) {
-        if (P.accumulate) old = load_cols<T, VEC>(static_cast<const T*>(P.dtable) + (int64_t)key * P.dim, col0, lane, P.dim);
+        if (P.accumulate) old = load_cols<T, VEC>(static_cast<const T*>(P.dtable), key, P.vocab, col0, lane, P.dim);
         add_part(part_at(P, chunk, 1, slab, lane), acc);
       }
 #pragma unroll 8

@@ -6,8 +6,7 @@
 // times.  Here a row stays in registers from y to z: x and y are read once, r and z written once (four row passes
 // forward; six backward: dr, dz, r, y in, dx, dy out).  What bounds both is memory.
 //
-// A row is held by a group of threads, eight consecutive elements each (or one element every group-width where rows are
-// not 16-byte aligned), NV such pieces a thread.  A group is one warp for short rows, else the whole CTA; CTAs are
+// A row is held by a group of threads, eight consecutive elements each, NV such pieces a thread.  A group is one warp for short rows, else the whole CTA; CTAs are
 // persistent, so parameters are read once per CTA and held in registers, and the next rows are on their way to shared memory
 // while a row is summed (three rows ahead at 4096 columns: 96 KB in flight an SM).  Mean and variance are taken in two passes over the registers: no cancellation.
 //
@@ -45,13 +44,9 @@ struct NormParams {
   float eps, a, b;
 };
 
-// The element numbers of a thread: piece j, k-th of eight.
-template <int VEC>
-__device__ __forceinline__ int col_of(int tid, int group, int j, int k) {
-  return VEC ? (tid + j * group) * 8 + k : tid + (j * 8 + k) * group;
-}
-
-// A row's pieces in a thread's registers.  Rows whose pieces are 16-byte words pass through shared memory, P.slots - 1 rows
+// The element numbers of a thread: k-th of eight of piece j.
+__device__ __forceinline__ int col_of(int tid, int group, int j, int k) { return (tid + j * group) * 8 + k; }
+// A row's pieces in a thread's registers.  Rows whose pieces are 16-byte words (VEC) pass through shared memory, P.slots - 1 rows
 // ahead.  A slot is an image of the row, and a warp copies just the part that its own threads read: no barrier wider than
 // the warp is needed.
 template <typename T, int VEC, int NV>
@@ -72,13 +67,13 @@ struct RowRegs {
       }
     }
   }
-  // From the slot, or (not VEC) from the row itself; pieces beyond dim are zeros.
-  __device__ __forceinline__ void load(const char* slot, const T* row, int tid, int group, int dim) {
+  // From the slot, or (not VEC) from the row itself, in [lo, hi); what lies beyond dim is zero.
+  __device__ __forceinline__ void load(const char* slot, const T* lo, int64_t at, const T* hi, int tid, int group, int dim) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       if (VEC) {
-        if (col_of<1>(tid, group, j, 0) < dim) {
+        if (col_of(tid, group, j, 0) < dim) {
           uint4* to = reinterpret_cast<uint4*>(&w[j]);
 #pragma unroll
           for (int q = 0; q < WORDS; ++q) to[q] = *reinterpret_cast<const uint4*>(slot + ((j * group + tid) * WORDS + q) * 16);
@@ -86,12 +81,8 @@ struct RowRegs {
           w[j].pack(v);
         }
       } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int c = col_of<0>(tid, group, j, k);
-          if (c < dim) v[k] = Elem<T>::get(row[c]);
-        }
-        w[j].pack(v);
+        const int c = col_of(tid, group, j, 0);
+        w[j] = load_any8(lo + at + c, there8(c, dim), lo, hi);
       }
     }
   }
@@ -107,46 +98,14 @@ __device__ __forceinline__ void fetch_wait(int rows) {
 }
 
 template <typename T, int VEC, int NV>
-__device__ __forceinline__ void store_row(T* row, int tid, int group, int dim, const float (&v)[NV][8]) {
+__device__ __forceinline__ void store_row2(T* row, int tid, int group, int dim, const f2_t (&v)[NV][4]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (VEC) {
-      const int c = col_of<1>(tid, group, j, 0);
-      if (c < dim) {
-        Raw8<T> o;
-        o.pack(v[j]);
-        store_raw8(row + c, o);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = col_of<0>(tid, group, j, k);
-        if (c < dim) row[c] = Elem<T>::put(v[j][k]);
-      }
-    }
-  }
-}
-
-// The same from pairs of elements.
-template <typename T, int VEC, int NV>
-__device__ __forceinline__ void store_row2(T* row, int tid, int group, int dim, const f2_t (&v)[NV][4]) {
-  if (VEC) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = col_of<1>(tid, group, j, 0);
-      if (c < dim) {
-        Raw8<T> o;
-        o.pack2(v[j]);
-        store_raw8(row + c, o);
-      }
-    }
-  } else {
-    float x[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) f2_unpack(v[j][k], x[j][2 * k], x[j][2 * k + 1]);
-    store_row<T, 0, NV>(row, tid, group, dim, x);
+    const int c = col_of(tid, group, j, 0);
+    Raw8<T> o;
+    o.pack2(v[j]);
+    if (!VEC) store_any8(row + c, there8(c, dim), o);
+    else if (c < dim) store_raw8(row + c, o);
   }
 }
 
@@ -156,7 +115,7 @@ __device__ __forceinline__ void load_param(const void* p, int dtype, float none,
   if (VEC && p && ((uintptr_t)p & 15) == 0) {  // whole pieces as 16-byte words
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = col_of<1>(tid, group, j, 0);
+      const int c = col_of(tid, group, j, 0);
       if (c >= dim) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
@@ -172,7 +131,7 @@ __device__ __forceinline__ void load_param(const void* p, int dtype, float none,
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int c = col_of<VEC>(tid, group, j, k);
+      const int c = col_of(tid, group, j, k);
       v[j][k] = c < dim ? param_at(p, c, dtype, none) : 0.0f;
     }
 }
@@ -228,12 +187,12 @@ __device__ __forceinline__ float2 row_stats(f2_t (&v)[NV][4], float eps, float i
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (VEC) {
-          if (col_of<1>(tid, group, j, 0) < dim) v[j][k] = f2_add(v[j][k], less);
+          if (col_of(tid, group, j, 0) < dim) v[j][k] = f2_add(v[j][k], less);
         } else {
           float a, b;
           f2_unpack(v[j][k], a, b);
-          v[j][k] = f2_pack(col_of<0>(tid, group, j, 2 * k) < dim ? a - mean : 0.0f,
-                            col_of<0>(tid, group, j, 2 * k + 1) < dim ? b - mean : 0.0f);
+          v[j][k] = f2_pack(col_of(tid, group, j, 2 * k) < dim ? a - mean : 0.0f,
+                            col_of(tid, group, j, 2 * k + 1) < dim ? b - mean : 0.0f);
         }
       }
     sum = f2_both(0.0f);
@@ -326,13 +285,13 @@ __global__ void __launch_bounds__(NORM_THREADS, NV == 1 && !BIAS ? 2 : 1) norm_k
     f2_t r[NV][4];
     {
       RowS xr;
-      xr.load(here + at_x, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
+      xr.load(here + at_x, static_cast<const TS*>(P.x), row * dim, static_cast<const TS*>(P.x) + P.rows * dim, tid, group, dim);
 #pragma unroll
       for (int j = 0; j < NV; ++j) xr.w[j].unpack2(r[j]);
     }
     if (P.y) {
       RowB yr;
-      yr.load(here, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+      yr.load(here, static_cast<const TB*>(P.y), row * dim, static_cast<const TB*>(P.y) + P.rows * dim, tid, group, dim);
       f2_t v[NV][4];
 #pragma unroll
       for (int j = 0; j < NV; ++j) yr.w[j].unpack2(v[j]);
@@ -455,10 +414,10 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
     if (++slot == P.slots) slot = 0;
     f2_t D[NV][4];
     RowB yr;
-    if (has_y && !VEC) yr.load(here, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+    if (has_y && !VEC) yr.load(here, static_cast<const TB*>(P.y), row * dim, static_cast<const TB*>(P.y) + P.rows * dim, tid, group, dim);
     if (P.dr) {
       RowS w;
-      w.load(here + at_dr, static_cast<const TS*>(P.dr) + row * dim, tid, group, dim);
+      w.load(here + at_dr, static_cast<const TS*>(P.dr), row * dim, static_cast<const TS*>(P.dr) + P.rows * dim, tid, group, dim);
 #pragma unroll
       for (int j = 0; j < NV; ++j) w.w[j].unpack2(D[j]);
     } else {
@@ -470,8 +429,8 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
     if (P.pre) {
       RowB zr;
       RowS rr;
-      zr.load(here + at_dz, static_cast<const TB*>(P.dz) + row * dim, tid, group, dim);
-      rr.load(here + at_r, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
+      zr.load(here + at_dz, static_cast<const TB*>(P.dz), row * dim, static_cast<const TB*>(P.dz) + P.rows * dim, tid, group, dim);
+      rr.load(here + at_r, static_cast<const TS*>(P.x), row * dim, static_cast<const TS*>(P.x) + P.rows * dim, tid, group, dim);
       const f2_t less = f2_both(-pre.x), rstd = f2_both(pre.y);
       f2_t v[NV][4], h[NV][4], s1 = f2_both(0.0f), s0 = f2_both(0.0f);
 #pragma unroll
@@ -503,7 +462,7 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
         }
     }
     if (has_y) {
-      if (VEC) yr.load(here, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+      if (VEC) yr.load(here, static_cast<const TB*>(P.y), row * dim, static_cast<const TB*>(P.y) + P.rows * dim, tid, group, dim);
       const f2_t less = f2_both(-post.x), rstd = f2_both(post.y), gate = f2_both(gt);
       f2_t v[NV][4], h[NV][4], s1 = f2_both(0.0f), s0 = f2_both(0.0f);
       float s2 = 0.0f;
@@ -527,7 +486,7 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int c = col_of<VEC>(tid, group, j, k);
+            const int c = col_of(tid, group, j, k);
             float d[2];
             f2_unpack(D[j][k >> 1], d[0], d[1]);
             if (c < dim) s2 = fmaf(d[k & 1], bias[c], s2);
@@ -573,7 +532,7 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int c = col_of<VEC>(tid, group, j, k);
+        const int c = col_of(tid, group, j, k);
         float x[2];
         f2_unpack(sum[j][k >> 1], x[0], x[1]);
         if (c < dim) p[c] = x[k & 1];

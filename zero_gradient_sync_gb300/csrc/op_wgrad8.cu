@@ -160,20 +160,17 @@ __device__ __forceinline__ Item item_at(const WgradParams& P, int32_t item) {
 
 // Up to 32 rows of one column of a warp's block to memory.  Adding in fp32 is left to the L2: each element gets one
 // addition a call, so nothing depends on an order, and nobody waits for the old value.  bf16 has to be added in fp32 and
-// rounded once, so its old values are read, 8 rows in flight.
+// rounded once, so its old values are read, all 32 rows in flight (the sums of the block are in shared memory by then).
 __device__ __forceinline__ void store_block(const WgradParams& P, int32_t part, int32_t row0, int32_t col0, int32_t r0,
                                             int32_t c, const float* block, int rows) {
   if (part < 0 && P.dtype == DP_BF16) {
     bf16_t* dst = static_cast<bf16_t*>(P.dw) + (int64_t)(row0 + r0) * P.k + col0 + c;
-    for (int i = 0; i < rows; i += 8) {
-      float old[8];
+    uint16_t old[32];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) old[r] = P.accumulate && i + r < rows ? bf16_to_f32(dst[r * P.k]) : 0.0f;
+    for (int r = 0; r < 32; ++r) old[r] = P.accumulate && r < rows ? dst[r * P.k] : (uint16_t)0;
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (i + r < rows) dst[r * P.k] = bf16_rn(__fadd_rn(old[r], block[(i + r) * 33]));
-      dst += 8 * P.k;
-    }
+    for (int r = 0; r < 32; ++r)
+      if (r < rows) dst[r * P.k] = bf16_rn(__fadd_rn(bf16_to_f32(old[r]), block[r * 33]));
     return;
   }
   const int64_t ld = part >= 0 ? BN : P.k;
@@ -378,9 +375,15 @@ __global__ void __launch_bounds__(BN) wgrad8_join_kernel(const __grid_constant__
     if (col + i < P.k) grad_put(P.dw, row * P.k + col + i, P.dtype, P.accumulate, v[i]);
 }
 
-// dy with rows that TMA cannot read, to rows of ld elements (a multiple of 8).
-__global__ void __launch_bounds__(256) wgrad8_copy_kernel(uint16_t* dst, int64_t ld, const uint16_t* src, int64_t lds, int64_t n) {
-  for (int64_t c = threadIdx.x; c < n; c += blockDim.x) dst[blockIdx.x * ld + c] = src[blockIdx.x * lds + c];
+// dy with rows that TMA cannot read, to rows of ld elements (a multiple of 8): a warp a row.
+__global__ void __launch_bounds__(256) wgrad8_copy_kernel(uint16_t* dst, int64_t ld, const uint16_t* src, int64_t lds, int64_t rows,
+                                                          int64_t n) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const uint16_t* end = src + (rows - 1) * lds + n;
+#pragma unroll 4
+  for (int64_t c = lane * 8; c < n; c += 256) store_raw8(dst + row * ld + c, load_any8(src + row * lds + c, there8(c, n), src, end));
 }
 
 // ---------------------------------------------------------------------------------------------------- host side
@@ -509,7 +512,7 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
   DP_TRY(dp_ckpt8_decode(base, codes, scales, rows, pitch, pitch, DP_BF16, stream_));
   int launches = 1;
   if (!aligned) {
-    wgrad8_copy_kernel<<<(unsigned)rows, 256, 0, stream>>>(reinterpret_cast<uint16_t*>(base + w.dy), w.lddy, dy, lddy, n);
+    wgrad8_copy_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(reinterpret_cast<uint16_t*>(base + w.dy), w.lddy, dy, lddy, rows, n);
     ++launches;
   }
   WgradParams P = {};
