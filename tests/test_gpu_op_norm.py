@@ -35,7 +35,7 @@ def d64(t):
 
 
 SHAPES = [(1, 1, 0), (5, 8, 0), (3, 77, 0), (7, 768, 0), (130, 264, 8), (9, 2048, 1), (33, 4096, 0), (3, 5000, 0), (2, 11008, 0),
-          (2, 16384, 0), (2, 16383, 0)]
+          (2, 16384, 0), (2, 16383, 0), (37, 60, 1), (21, 128, 0), (50, 100, 3), (19, 24, 0)]
 
 
 @pytest.mark.parametrize("kind", ["rms", "layer"])

@@ -11,8 +11,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdpstep.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["dp_api.cu", "dp_kernels.cu", "dp_static.cu", "dp_checkpoint.cu", "dp_tree.cu", "dp_tree_sp.cu",
-           "dp_micro.cu", "op_embedding.cu", "op_norm.cu", "op_ckpt8.cu", "op_wgrad8.cu"]
-HEADERS = ["dp_device.cuh", "dp_internal.h", "dp_launch.h", "dp_single.cuh", "op_common.cuh"]
+           "dp_micro.cu", "op_embedding.cu", "op_norm.cu", "op_norm_grad.cu",
+           "op_ckpt8.cu", "op_wgrad8.cu"]
+HEADERS = ["dp_device.cuh", "dp_internal.h", "dp_launch.h", "dp_single.cuh", "op_common.cuh", "op_norm.cuh"]
 PUBLIC = ["dpstep.h", "dpops.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")

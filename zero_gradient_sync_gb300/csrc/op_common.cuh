@@ -143,45 +143,52 @@ __device__ __forceinline__ void shift_words(uint32_t (&w)[N], uint32_t by, uint3
   for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i], i + 1 < N ? w[i + 1] : 0u, (by & 2) * 8);
 }
 
-// The first n (0..8) elements at p, zeros behind them.  Whole 16-byte words are read where they lie inside [lo, hi), the
-// tensor; the others' elements one by one.
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_any8(const T* p, int n, const T* lo, const T* hi) {
+// The first n (0..8) elements from byte `by` on of words that hold them, zeros behind them.
+template <typename T, int N>
+__device__ __forceinline__ Raw8<T> take8(uint32_t (&w)[N], uint32_t by, int n) {
   constexpr int WORDS = sizeof(T) * 2;  // 32-bit words of eight elements
   uint32_t out[WORDS];
+  shift_words(w, by, out);
+  if (n < 8) {
 #pragma unroll
-  for (int i = 0; i < WORDS; ++i) out[i] = 0;
-  const uint32_t s = (uint32_t)(uintptr_t)p & 15u;
-  const char* first = reinterpret_cast<const char*>(p) - s;
-  const uint32_t need = s + (uint32_t)n * sizeof(T);  // bytes from `first`
-  const uint32_t whole = (need + 15u) & ~15u;
-  if (n > 0 && first >= reinterpret_cast<const char*>(lo) && first + whole <= reinterpret_cast<const char*>(hi)) {
-    uint32_t w[WORDS + 4];
-#pragma unroll
-    for (int q = 0; q <= WORDS / 4; ++q) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (need > 16u * q) x = *(reinterpret_cast<const uint4*>(first) + q);  // L1 has it for the next lane
-      w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
+    for (int i = 0; i < WORDS; ++i) {
+      const int left = n * (int)sizeof(T) - 4 * i;  // bytes of this word that count
+      out[i] &= left >= 4 ? 0xffffffffu : left == 2 ? 0xffffu : 0u;
     }
-    shift_words(w, s, out);
-    if (n < 8) {
-#pragma unroll
-      for (int i = 0; i < WORDS; ++i) {
-        const int left = n * (int)sizeof(T) - 4 * i;  // bytes of this word that count
-        out[i] &= left >= 4 ? 0xffffffffu : left == 2 ? 0xffffu : 0u;
-      }
-    }
-  } else {
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-    for (int i = 0; i < 2 * WORDS; ++i)
-      if (i * 2 < n * (int)sizeof(T)) out[i >> 1] |= (uint32_t)h[i] << (16 * (i & 1));
   }
   Raw8<T> r;
   uint32_t* to = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
   for (int i = 0; i < WORDS; ++i) to[i] = out[i];
   return r;
+}
+
+// The first n (0..8) elements at p, zeros behind them.  Whole 16-byte words are read where they lie inside [lo, hi), the
+// tensor; the others' elements one by one.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_any8(const T* p, int n, const T* lo, const T* hi) {
+  constexpr int WORDS = sizeof(T) * 2;
+  const uint32_t s = (uint32_t)(uintptr_t)p & 15u;
+  const char* first = reinterpret_cast<const char*>(p) - s;
+  const uint32_t need = s + (uint32_t)n * sizeof(T);  // bytes from `first`
+  const uint32_t whole = (need + 15u) & ~15u;
+  uint32_t w[WORDS + 4];
+#pragma unroll
+  for (int i = 0; i < WORDS + 4; ++i) w[i] = 0;
+  if (n > 0 && first >= reinterpret_cast<const char*>(lo) && first + whole <= reinterpret_cast<const char*>(hi)) {
+#pragma unroll
+    for (int q = 0; q <= WORDS / 4; ++q) {
+      if (need <= 16u * q) continue;
+      const uint4 x = *(reinterpret_cast<const uint4*>(first) + q);  // L1 has it for the next lane
+      w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
+    }
+    return take8<T>(w, s, n);
+  }
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 2 * WORDS; ++i)
+    if (i * 2 < n * (int)sizeof(T)) w[i >> 1] |= (uint32_t)h[i] << (16 * (i & 1));
+  return take8<T>(w, 0, n);
 }
 
 // Writes the first n (0..8) elements of r to p; called by whole warps.  Where the next lane's elements follow this lane's in

@@ -1,0 +1,324 @@
+// Shared by the norms around a block (op_norm.cu) and their gradient (op_norm_grad.cu): rows in registers, sums over a group of
+// threads, launch plans, argument checks.
+#pragma once
+
+#include <math.h>
+
+#include <initializer_list>
+
+#include "op_common.cuh"
+
+namespace dp {
+namespace {
+
+constexpr int NORM_THREADS = 512;   // most threads of a group
+constexpr int MAX_PARTS = 1024;     // most CTAs (partial rows) of the gradient
+constexpr int FIN_COLS = 16, FIN_ROWS = 64;
+constexpr int MAX_SLOTS = 4;
+
+struct NormParams {
+  void *r, *z, *dx, *dy, *dgate_token;
+  const void *x, *y, *dr, *dz;
+  const void *w_post, *b_post, *gate, *w_pre, *b_pre;
+  float2 *post_stats, *pre_stats;
+  float* part;
+  int64_t rows;
+  int dim, group, per_cta, slots;  // threads of a row, rows of a CTA at a time, rows in flight
+  int layer, post, pre, gate_mode, pdt, accumulate, bias;
+  float eps, a, b;
+};
+
+// The element numbers of a thread: k-th of eight of piece j.
+__device__ __forceinline__ int col_of(int tid, int group, int j, int k) { return (tid + j * group) * 8 + k; }
+// A row's pieces in a thread's registers.  Rows whose pieces are 16-byte words (VEC) pass through shared memory, P.slots - 1 rows
+// ahead.  A slot is an image of the row, and a warp copies just the part that its own threads read: no barrier wider than
+// the warp is needed.
+template <typename T, int VEC, int NV>
+struct RowRegs {
+  static constexpr int WORDS = sizeof(T) / 2;  // 16-byte words of eight elements
+  Raw8<T> w[NV];
+  static __device__ __forceinline__ int bytes(int group) { return NV * group * 16 * WORDS; }
+  static __device__ __forceinline__ void fetch(char* slot, const T* row, int tid, int group, int dim) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int q = 0; q < WORDS; ++q) {  // neighbours copy neighbouring words
+        const int part = group < 32 ? group : 32, lane = tid & (part - 1);
+        const int at = (j * group + tid - lane) * 16 * WORDS + (q * part + lane) * 16;
+        if (at < dim * (int)sizeof(T))
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot + at)),
+                       "l"(reinterpret_cast<const char*>(row) + at)
+                       : "memory");
+      }
+    }
+  }
+  // From the slot, or (not VEC) from the row itself, in [lo, hi); what lies beyond dim is zero.
+  __device__ __forceinline__ void load(const char* slot, const T* lo, int64_t at, const T* hi, int tid, int group, int dim) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (VEC) {
+        if (col_of(tid, group, j, 0) < dim) {
+          uint4* to = reinterpret_cast<uint4*>(&w[j]);
+#pragma unroll
+          for (int q = 0; q < WORDS; ++q) to[q] = *reinterpret_cast<const uint4*>(slot + ((j * group + tid) * WORDS + q) * 16);
+        } else {
+          w[j].pack(v);
+        }
+      } else {
+        const int c = col_of(tid, group, j, 0);
+        w[j] = load_any8(lo + at + c, there8(c, dim), lo, hi);
+      }
+    }
+  }
+};
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but the last `rows` fetched rows are there.
+__device__ __forceinline__ void fetch_wait(int rows) {
+  if (rows == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (rows == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (rows == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+}
+
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void store_row2(T* row, int tid, int group, int dim, const f2_t (&v)[NV][4]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = col_of(tid, group, j, 0);
+    Raw8<T> o;
+    o.pack2(v[j]);
+    if (!VEC) store_any8(row + c, there8(c, dim), o);
+    else if (c < dim) store_raw8(row + c, o);
+  }
+}
+
+template <int VEC, int NV>
+__device__ __forceinline__ void load_param(const void* p, int dtype, float none, int tid, int group, int dim,
+                                           float (&v)[NV][8]) {
+  if (VEC && p && ((uintptr_t)p & 15) == 0) {  // whole pieces as 16-byte words
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = col_of(tid, group, j, 0);
+      if (c >= dim) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
+      } else if (dtype == DP_BF16) {
+        load_raw8(static_cast<const bf16_t*>(p) + c).unpack(v[j]);
+      } else {
+        load_raw8(static_cast<const float*>(p) + c).unpack(v[j]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = col_of(tid, group, j, k);
+      v[j][k] = c < dim ? param_at(p, c, dtype, none) : 0.0f;
+    }
+}
+
+// Sums of N values over a group of threads; every thread gets them.  A CTA-wide group alternates between two halves of
+// `buf` (zero beyond the group's warps), so one barrier a call is enough: a half is written again only after the barrier
+// of the call in between.  The warps' sums are read as broadcast words, which takes less than another five shuffles.
+typedef float GroupBuf[2][3][16];
+template <int N, bool SMALL>
+__device__ __forceinline__ void group_sum(float (&v)[N], int group, GroupBuf& buf, int& half) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (!SMALL || o < group) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
+  if (SMALL) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) buf[half][i][warp] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float4* p = reinterpret_cast<const float4*>(buf[half][i]);
+    const float4 a = p[0], b = p[1], c = p[2], d = p[3];
+    v[i] = (((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w))) + (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
+  }
+  half ^= 1;
+}
+__device__ __forceinline__ void clear(GroupBuf& buf) {
+  for (int i = threadIdx.x; i < 96; i += blockDim.x) (&buf[0][0][0])[i] = 0.0f;
+  __syncthreads();
+}
+
+// Mean (0 for RMS) and 1 / sqrt(var + eps) of a row held in registers, which is centred on the way.  Pieces beyond dim hold
+// zeros, before and after.
+template <int VEC, int NV, bool LAYER, bool SMALL>
+__device__ __forceinline__ float2 row_stats(f2_t (&v)[NV][4], float eps, float inv, int tid, int group, int dim, GroupBuf& buf,
+                                            int& half) {
+  float s[1], mean = 0.0f;
+  f2_t sum = f2_both(0.0f);
+  if (LAYER) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum = f2_add(sum, v[j][k]);
+    s[0] = f2_sum(sum);
+    group_sum<1, SMALL>(s, group, buf, half);
+    mean = s[0] * inv;
+    const f2_t less = f2_both(-mean);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (VEC) {
+          if (col_of(tid, group, j, 0) < dim) v[j][k] = f2_add(v[j][k], less);
+        } else {
+          float a, b;
+          f2_unpack(v[j][k], a, b);
+          v[j][k] = f2_pack(col_of(tid, group, j, 2 * k) < dim ? a - mean : 0.0f,
+                            col_of(tid, group, j, 2 * k + 1) < dim ? b - mean : 0.0f);
+        }
+      }
+    sum = f2_both(0.0f);
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum = f2_fma(v[j][k], v[j][k], sum);
+  s[0] = f2_sum(sum);
+  group_sum<1, SMALL>(s, group, buf, half);
+  return make_float2(mean, 1.0f / sqrtf(fmaf(s[0], inv, eps)));
+}
+
+// The kernels' PIECES is NV, or 0 for SMALL groups with one piece.
+
+// ---------------------------------------------------------------------------------------------------- host side
+
+// Pieces of eight a thread holds: one up to 4096 columns, so that a row has as many threads as it can use.
+int pieces_of(int dim) { return dim <= NORM_THREADS * 8 ? 1 : dim <= NORM_THREADS * 16 ? 2 : 4; }
+
+struct Shape {
+  int nv, group, per_cta, threads;
+};
+Shape shape_of(int dim) {
+  Shape s;
+  s.nv = pieces_of(dim);
+  s.group = dim <= 64 ? 8 : dim <= 128 ? 16 : (dim + s.nv * 8 * 32 - 1) / (s.nv * 8 * 32) * 32;
+  s.per_cta = s.group <= 32 ? 128 / s.group : 1;
+  s.threads = s.group * s.per_cta;
+  return s;
+}
+
+// Rows in flight, and with that the shared memory, of a kernel whose CTAs take `set` bytes a row: four where all CTAs that the
+// registers allow an SM still fit, fewer for long rows.  A kernel's last answer is kept: asking takes longer than a launch.
+struct Plan1 {
+  int device = -1, threads = 0, slots = 1, ctas = 0;  // ctas: one wave
+  int64_t set = -1, more = -1;
+};
+template <typename K>
+void plan_of(K kernel, int threads, int64_t set, int64_t more, Plan1& c) {
+  int device = 0;
+  cudaGetDevice(&device);
+  if (c.device == device && c.threads == threads && c.set == set && c.more == more) return;
+  c.slots = 1;
+  int per_sm = 1;
+  if (set > 0) {
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+    const int64_t room = 220 * 1024;
+    if (per_sm < 1) per_sm = 1;
+    while (per_sm > 1 && per_sm * (set * 2 + more) > room) --per_sm;
+    const int64_t n = (room / per_sm - more) / set;
+    c.slots = (int)(n < 1 ? 1 : n > MAX_SLOTS ? MAX_SLOTS : n);
+  }
+  const size_t smem = (size_t)(c.slots * set + more);
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  c.ctas = occupancy_grid(kernel, threads, smem, INT32_MAX);
+  c.device = device;
+  c.threads = threads;
+  c.set = set;
+  c.more = more;
+}
+template <typename K>
+int launch_rows(K kernel, Plan1& c, const Shape& s, NormParams& P, int64_t set, int64_t more, int most, cudaStream_t stream) {
+  plan_of(kernel, s.threads, set, more, c);
+  P.slots = c.slots;
+  const int64_t want = (P.rows + s.per_cta - 1) / s.per_cta;
+  int64_t grid = want < c.ctas ? want : c.ctas;
+  if (grid > most) grid = most;
+  kernel<<<(unsigned)grid, s.threads, (size_t)(c.slots * set + more), stream>>>(P);
+  return (int)grid;
+}
+
+// f(stream type, block type, VEC, NV) for the sizes and types of one call.
+template <typename F>
+auto dispatch(const dp_block_norm_t& p, bool vec, int nv, F&& f) {
+#define DP_NV(TS, TB, V) \
+  (nv == 0 ? f.template operator()<TS, TB, V, 0>() : nv == 1 ? f.template operator()<TS, TB, V, 1>() : nv == 2 ? f.template operator()<TS, TB, V, 2>() \
+                                                             : f.template operator()<TS, TB, V, 4>())
+#define DP_VEC(TS, TB) (vec ? DP_NV(TS, TB, 1) : DP_NV(TS, TB, 0))
+  if (p.stream_dtype == DP_BF16) return DP_VEC(bf16_t, bf16_t);
+  if (p.block_dtype == DP_BF16) return DP_VEC(float, bf16_t);
+  return DP_VEC(float, float);
+#undef DP_VEC
+#undef DP_NV
+}
+
+dp_status_t check_norm(const dp_block_norm_t* p, bool has_y, bool gate) {
+  if (!p) return op_fail(DP_ERR_INVALID_ARG, "p is NULL");
+  if (p->rows < 0 || p->rows > INT32_MAX) return op_fail(DP_ERR_INVALID_ARG, "rows = %lld not in 0..2^31-1", (long long)p->rows);
+  if (p->dim < 1 || p->dim > DP_MAX_NORM_DIM) return op_fail(DP_ERR_INVALID_ARG, "dim = %d not in 1..%d", p->dim, DP_MAX_NORM_DIM);
+  if (p->kind != DP_NORM_RMS && p->kind != DP_NORM_LAYER) return op_fail(DP_ERR_INVALID_ARG, "kind = %d unknown", p->kind);
+  if (p->norms & ~(DP_NORM_POST | DP_NORM_PRE)) return op_fail(DP_ERR_INVALID_ARG, "norms = %d unknown", p->norms);
+  if (p->gate_mode < DP_GATE_NONE || p->gate_mode > DP_GATE_TOKEN) return op_fail(DP_ERR_INVALID_ARG, "gate_mode = %d unknown", p->gate_mode);
+  DP_TRY(check_dtype(p->stream_dtype, "stream_dtype"));
+  DP_TRY(check_dtype(p->block_dtype, "block_dtype"));
+  DP_TRY(check_dtype(p->param_dtype, "param_dtype"));
+  if (p->stream_dtype == DP_BF16 && p->block_dtype == DP_F32)
+    return op_fail(DP_ERR_INVALID_ARG, "fp32 block tensors need an fp32 stream");
+  if (p->accumulate != 0 && p->accumulate != 1) return op_fail(DP_ERR_INVALID_ARG, "accumulate = %d is neither 0 nor 1", p->accumulate);
+  if (!(p->eps > 0.0f) || !(p->eps < 1e30f)) return op_fail(DP_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (!(fabsf(p->res_scale) < 1e30f) || !(fabsf(p->branch_scale) < 1e30f))
+    return op_fail(DP_ERR_INVALID_ARG, "res_scale and branch_scale must be finite");
+  if (p->rows == 0) return DP_OK;  // empty tensors have no address: nothing says which of them are there
+  if ((p->gate_mode != DP_GATE_NONE) != gate)
+    return op_fail(DP_ERR_INVALID_ARG, "gate and gate_mode disagree");
+  if (!has_y && (p->norms & DP_NORM_POST || gate || p->res_scale != 1.0f))
+    return op_fail(DP_ERR_INVALID_ARG, "without y there is no post norm, no gate and res_scale is 1");
+  if (!has_y && !(p->norms & DP_NORM_PRE)) return op_fail(DP_ERR_INVALID_ARG, "neither a block output nor a norm before the next block");
+  return DP_OK;
+}
+
+NormParams base_params(const dp_block_norm_t& p, const Shape& s) {
+  NormParams P = {};
+  P.rows = p.rows;
+  P.dim = p.dim;
+  P.group = s.group;
+  P.per_cta = s.per_cta;
+  P.layer = p.kind == DP_NORM_LAYER;
+  P.post = (p.norms & DP_NORM_POST) != 0;
+  P.pre = (p.norms & DP_NORM_PRE) != 0;
+  P.gate_mode = p.gate_mode;
+  P.pdt = p.param_dtype;
+  P.accumulate = p.accumulate;
+  P.eps = p.eps;
+  P.a = p.res_scale;
+  P.b = p.branch_scale;
+  return P;
+}
+
+// Whether one row of a CTA fits its shared memory (`pairs` rows of the stream and of the block).
+bool slots_fit(const dp_block_norm_t& p, const Shape& s, int pairs) {
+  return (int64_t)s.threads * s.nv * 8 * pairs * (elem_size(p.stream_dtype) + elem_size(p.block_dtype)) + 4 * p.dim <= 220 * 1024;
+}
+
+bool all16(std::initializer_list<const void*> ps) {
+  for (const void* q : ps)
+    if (!is_aligned(q, 16)) return false;
+  return true;
+}
+
+}  // namespace
+}  // namespace dp

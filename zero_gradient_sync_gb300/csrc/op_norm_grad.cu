@@ -1,0 +1,427 @@
+// The gradient of the norms around a block (op_norm.cu).
+//
+// Gradient, with yh, rh the rows before weights and biases, D = dr + N_pre'(dz) and q = g D for a gate per token, else D:
+//   v  = w_pre dz:      D  = dr + rstd_pre (v - rh mean(v rh) - mean(v))          (RMS: without mean(v))
+//   v' = b g w_post D:  dy = rstd_post (v' - yh mean(v' yh) - mean(v')),   dx = a D
+//   P1 = sum dz rh, P0 = sum dz, S1 = sum q yh, S0 = sum q   over the rows, for each column
+//   dw_pre = P1, db_pre = P0, dw_post = b g S1, db_post = b g S0, dgate = b (w_post S1 + c_post S0) for a gate per
+//   channel; for one per token, dgate = b (sum over the row of D (w_post yh + c_post)).
+// So all five parameter gradients come from four column sums (two for RMS norms without biases), kept in registers over
+// the rows of a CTA, left in the workspace as one partial row a CTA, and added in CTA order by a second kernel.
+#include "op_norm.cuh"
+
+namespace dp {
+namespace {
+
+// LAYER: rows are centred.  SUM0: some gradient needs S0 or P0 (a bias is there).  The workspace holds, for each group of
+// threads, S1 and P1 and (SUM0) S0 and P0, dim floats each.
+template <typename TS, typename TB, int VEC, int PIECES, bool LAYER, bool SUM0>
+__global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_constant__ NormParams P) {
+  constexpr bool SMALL = PIECES == 0;
+  constexpr int NV = SMALL ? 1 : PIECES;
+  extern __shared__ __align__(128) char slots[];
+  __shared__ __align__(16) GroupBuf buf;
+  clear(buf);
+  typedef RowRegs<TS, VEC, NV> RowS;
+  typedef RowRegs<TB, VEC, NV> RowB;
+  int half = 0;
+  const int tid = SMALL ? threadIdx.x & (P.group - 1) : threadIdx.x, which = SMALL ? threadIdx.x / P.group : 0;  // of the CTA's groups
+  const int per_cta = SMALL ? P.per_cta : 1;
+  const int64_t row0 = (int64_t)blockIdx.x * per_cta + which, step = (int64_t)gridDim.x * per_cta;
+  const int group = P.group, dim = P.dim;
+  const int at_dz = RowB::bytes(group), at_r = 2 * at_dz, at_dr = at_r + RowS::bytes(group);
+  const int slot_bytes = at_dr + RowS::bytes(group);
+  char* mine = slots + which * P.slots * slot_bytes;
+  auto fetch = [&](int64_t row, int slot) {
+    if (VEC) __syncwarp();  // the slot's last row has been read
+    if (VEC && row < P.rows) {
+      char* to = mine + slot * slot_bytes;
+      if (P.y) RowB::fetch(to, static_cast<const TB*>(P.y) + row * dim, tid, group, dim);
+      if (P.pre) {
+        RowB::fetch(to + at_dz, static_cast<const TB*>(P.dz) + row * dim, tid, group, dim);
+        RowS::fetch(to + at_r, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
+      }
+      if (P.dr) RowS::fetch(to + at_dr, static_cast<const TS*>(P.dr) + row * dim, tid, group, dim);
+    }
+    if (VEC) fetched();
+  };
+  grid_go();
+  for (int s = 0; s + 1 < P.slots; ++s) fetch(row0 + s * step, s);
+  int slot = 0;
+  // For the gradient of a gate per token: the post norm's bias, read for every row.
+  float* bias = reinterpret_cast<float*>(slots + (VEC ? per_cta * P.slots * slot_bytes : 0));
+  if (P.bias) {
+    for (int c = threadIdx.x; c < dim; c += blockDim.x) bias[c] = param_at(P.b_post, c, P.pdt, 0.0f);
+    __syncthreads();
+  }
+  const bool has_y = P.y != nullptr, token = P.gate_mode == DP_GATE_TOKEN;
+  f2_t A[NV][4], wp[NV][4];  // b g w_post, w_pre
+  f2_t S1[NV][4], P1[NV][4], S0[NV][4], P0[NV][4];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A[j][k] = wp[j][k] = S1[j][k] = P1[j][k] = S0[j][k] = P0[j][k] = f2_both(0.0f);
+  {
+    float v[NV][8];
+    if (has_y) {
+      load_param<VEC, NV>(P.w_post, P.pdt, 1.0f, tid, group, dim, v);
+      float g[NV][8];
+      load_param<VEC, NV>(P.gate_mode == DP_GATE_CHANNEL ? P.gate : nullptr, P.pdt, 1.0f, tid, group, dim, g);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          v[j][k] *= P.b * g[j][k];
+          if (k & 1) A[j][k >> 1] = f2_pack(v[j][k - 1], v[j][k]);
+        }
+    }
+    if (P.pre) {
+      load_param<VEC, NV>(P.w_pre, P.pdt, 1.0f, tid, group, dim, v);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) wp[j][k] = f2_pack(v[j][2 * k], v[j][2 * k + 1]);
+    }
+  }
+  const float inv = 1.0f / (float)dim;
+  // The next row's statistics are loaded a row ahead, like its elements.
+  float2 next_pre = make_float2(0.0f, 1.0f), next_post = make_float2(0.0f, 1.0f);
+  uint32_t next_gate = P.pdt == DP_BF16 ? 0x3f80u : 0x3f800000u;  // as it lies in memory: a conversion would wait for it
+  auto scalars = [&](int64_t row) {
+    if (row >= P.rows) return;
+    if (P.pre) next_pre = P.pre_stats[row];
+    if (P.post) next_post = P.post_stats[row];
+    if (token) next_gate = P.pdt == DP_BF16 ? __ldg(static_cast<const uint16_t*>(P.gate) + row) : __ldg(static_cast<const uint32_t*>(P.gate) + row);
+  };
+  scalars(row0);
+
+  // The groups of one warp go round equally often: one whose row is beyond the end goes along with a row of no elements.
+  for (int64_t row = row0; row - (SMALL ? which : 0) < P.rows; row += step) {
+    const bool live = !SMALL || row < P.rows;
+    const int row_dim = live ? dim : 0;
+    fetch(row + (P.slots - 1) * step, slot == 0 ? P.slots - 1 : slot - 1);
+    const float2 pre = next_pre, post = next_post;
+    const float gt = __uint_as_float(P.pdt == DP_BF16 ? next_gate << 16 : next_gate);
+    scalars(row + step);
+    if (VEC) fetch_wait(P.slots - 1);
+    const char* here = mine + slot * slot_bytes;
+    if (++slot == P.slots) slot = 0;
+    f2_t D[NV][4];
+    RowB yr;
+    if (has_y && !VEC) yr.load(here, static_cast<const TB*>(P.y), row * dim, static_cast<const TB*>(P.y) + P.rows * dim, tid, group, row_dim);
+    if (P.dr) {
+      RowS w;
+      w.load(here + at_dr, static_cast<const TS*>(P.dr), row * dim, static_cast<const TS*>(P.dr) + P.rows * dim, tid, group, row_dim);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) w.w[j].unpack2(D[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) D[j][k] = f2_both(0.0f);
+    }
+    if (P.pre) {
+      RowB zr;
+      RowS rr;
+      zr.load(here + at_dz, static_cast<const TB*>(P.dz), row * dim, static_cast<const TB*>(P.dz) + P.rows * dim, tid, group, row_dim);
+      rr.load(here + at_r, static_cast<const TS*>(P.x), row * dim, static_cast<const TS*>(P.x) + P.rows * dim, tid, group, row_dim);
+      const f2_t less = f2_both(-pre.x), rstd = f2_both(pre.y);
+      f2_t v[NV][4], h[NV][4], s1 = f2_both(0.0f), s0 = f2_both(0.0f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        zr.w[j].unpack2(v[j]);
+        rr.w[j].unpack2(h[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (LAYER) h[j][k] = f2_add(h[j][k], less);
+          h[j][k] = f2_mul(h[j][k], rstd);
+          P1[j][k] = f2_fma(v[j][k], h[j][k], P1[j][k]);
+          if (SUM0) P0[j][k] = f2_add(P0[j][k], v[j][k]);
+          v[j][k] = f2_mul(v[j][k], wp[j][k]);  // zero beyond dim
+          s1 = f2_fma(v[j][k], h[j][k], s1);
+          if (LAYER) s0 = f2_add(s0, v[j][k]);
+        }
+      }
+      float s[LAYER ? 2 : 1] = {f2_sum(s1)};
+      if (LAYER) s[LAYER ? 1 : 0] = f2_sum(s0);
+      group_sum<LAYER ? 2 : 1, SMALL>(s, group, buf, half);
+      const f2_t c1 = f2_both(-s[0] * inv), c0 = f2_both(LAYER ? -s[LAYER ? 1 : 0] * inv : 0.0f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f2_t x = f2_fma(h[j][k], c1, v[j][k]);
+          if (LAYER) x = f2_add(x, c0);
+          D[j][k] = f2_fma(x, rstd, D[j][k]);
+        }
+    }
+    if (has_y) {
+      if (VEC) yr.load(here, static_cast<const TB*>(P.y), row * dim, static_cast<const TB*>(P.y) + P.rows * dim, tid, group, row_dim);
+      const f2_t less = f2_both(-post.x), rstd = f2_both(post.y), gate = f2_both(gt);
+      f2_t v[NV][4], h[NV][4], s1 = f2_both(0.0f), s0 = f2_both(0.0f);
+      float s2 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        yr.w[j].unpack2(h[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (LAYER) h[j][k] = f2_add(h[j][k], less);
+          h[j][k] = f2_mul(h[j][k], rstd);
+          const f2_t q = f2_mul(gate, D[j][k]);
+          v[j][k] = f2_mul(A[j][k], D[j][k]);
+          S1[j][k] = f2_fma(q, h[j][k], S1[j][k]);
+          if (SUM0) S0[j][k] = f2_add(S0[j][k], q);
+          s1 = f2_fma(v[j][k], h[j][k], s1);
+          if (LAYER) s0 = f2_add(s0, v[j][k]);
+        }
+      }
+      if (P.bias) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int c = col_of(tid, group, j, k);
+            float d[2];
+            f2_unpack(D[j][k >> 1], d[0], d[1]);
+            if (c < dim) s2 = fmaf(d[k & 1], bias[c], s2);
+          }
+      }
+      float c1 = f2_sum(s1), c0 = LAYER ? f2_sum(s0) : 0.0f;
+      if (token) {
+        float s[3] = {c1, c0, s2};
+        group_sum<3, SMALL>(s, group, buf, half);
+        c1 = s[0];
+        c0 = s[1];
+        if (P.dgate_token && live && tid == 0) grad_put(P.dgate_token, row, P.pdt, P.accumulate, fmaf(P.b, s[2], s[0]));
+      } else if (P.post) {
+        float s[LAYER ? 2 : 1] = {c1};
+        if (LAYER) s[LAYER ? 1 : 0] = c0;
+        group_sum<LAYER ? 2 : 1, SMALL>(s, group, buf, half);
+        c1 = s[0];
+        if (LAYER) c0 = s[LAYER ? 1 : 0];
+      }
+      const f2_t m1 = f2_both(P.post ? -c1 * inv : 0.0f), m0 = f2_both(P.post ? -c0 * inv : 0.0f), f = f2_both(gt * post.y);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f2_t x = f2_fma(h[j][k], m1, v[j][k]);
+          if (LAYER) x = f2_add(x, m0);
+          h[j][k] = f2_mul(x, f);
+        }
+      store_row2<TB, VEC, NV>(static_cast<TB*>(P.dy) + row * dim, tid, group, row_dim, h);
+    }
+    const f2_t a = f2_both(P.a);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) D[j][k] = f2_mul(D[j][k], a);
+    store_row2<TS, VEC, NV>(static_cast<TS*>(P.dx) + row * dim, tid, group, row_dim, D);
+  }
+  // One partial row a CTA.  Where a CTA has several groups, their sums are added in shared memory first, in order.
+  __shared__ float together[SMALL ? 4 : 1][SMALL ? 256 : 1];
+  auto leave = [&](int q, const f2_t (&sum)[NV][4]) {
+    float* p = P.part + ((int64_t)blockIdx.x * (SUM0 ? 4 : 2) + q) * dim;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = col_of(tid, group, j, k);
+        float x[2];
+        f2_unpack(sum[j][k >> 1], x[0], x[1]);
+        if (c >= dim) continue;
+        if (!SMALL) p[c] = x[k & 1];
+        else together[q][c] = which == 0 ? x[k & 1] : together[q][c] + x[k & 1];
+      }
+  };
+  for (int g = 0; g < per_cta; ++g) {
+    if (g == which) {
+      leave(0, S1);
+      leave(1, P1);
+      if (SUM0) {
+        leave(2, S0);
+        leave(3, P0);
+      }
+    }
+    if (SMALL) __syncthreads();
+  }
+  if (SMALL) {
+    constexpr int ROWS = SUM0 ? 4 : 2;
+    for (int i = threadIdx.x; i < ROWS * dim; i += blockDim.x)
+      P.part[(int64_t)blockIdx.x * ROWS * dim + i] = together[i / dim][i % dim];
+  }
+}
+
+struct FinishParams {
+  const float* part;
+  int64_t parts;
+  int dim, sum0, gate_mode, pdt, accumulate;
+  const void *w_post, *b_post, *gate;
+  void *dw_post, *db_post, *dgate, *dw_pre, *db_pre;
+  float b;
+};
+
+// Adds the partial rows of 16 columns: 64 threads a column take the parts in turn, then a warp adds the 64 in a fixed order.
+__global__ void __launch_bounds__(FIN_COLS* FIN_ROWS) norm_finish_kernel(const __grid_constant__ FinishParams P) {
+  __shared__ float sums[4 * FIN_COLS][FIN_ROWS + 1];
+  __shared__ float done[4 * FIN_COLS];
+  grid_wait();
+  const int c0 = blockIdx.x * FIN_COLS + threadIdx.x;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c0 < P.dim) {
+#pragma unroll 5
+    for (int64_t i = threadIdx.y; i < P.parts; i += FIN_ROWS) {
+      const float* p = P.part + i * (P.sum0 ? 4 : 2) * P.dim + c0;
+      s[0] += p[0];
+      s[1] += p[P.dim];
+      if (P.sum0) {
+        s[2] += p[2 * (int64_t)P.dim];
+        s[3] += p[3 * (int64_t)P.dim];
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) sums[q * FIN_COLS + threadIdx.x][threadIdx.y] = s[q];
+  __syncthreads();
+  const int t = threadIdx.y * FIN_COLS + threadIdx.x, lane = t & 31;
+  for (int i = t >> 5; i < 4 * FIN_COLS; i += FIN_COLS * FIN_ROWS / 32) {
+    float v = sums[i][lane] + sums[i][lane + 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) done[i] = v;
+  }
+  __syncthreads();
+  const int c = blockIdx.x * FIN_COLS + t;
+  if (t >= FIN_COLS || c >= P.dim) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) s[q] = done[q * FIN_COLS + t];
+  const float g = P.b * (P.gate_mode == DP_GATE_CHANNEL ? param_at(P.gate, c, P.pdt, 1.0f) : 1.0f);
+  if (P.dw_post) grad_put(P.dw_post, c, P.pdt, P.accumulate, g * s[0]);
+  if (P.db_post) grad_put(P.db_post, c, P.pdt, P.accumulate, g * s[2]);
+  if (P.dgate)
+    grad_put(P.dgate, c, P.pdt, P.accumulate,
+             P.b * fmaf(param_at(P.w_post, c, P.pdt, 1.0f), s[0], param_at(P.b_post, c, P.pdt, 0.0f) * s[2]));
+  if (P.dw_pre) grad_put(P.dw_pre, c, P.pdt, P.accumulate, s[1]);
+  if (P.db_pre) grad_put(P.db_pre, c, P.pdt, P.accumulate, s[3]);
+}
+
+template <typename TS, typename TB, int VEC, int NV>
+int run_grad(NormParams P, const Shape& s, bool sum0, cudaStream_t stream) {
+  static thread_local Plan1 plan[3];
+  const int which = P.layer ? 2 : sum0 ? 1 : 0;
+  auto k = P.layer ? norm_grad_kernel<TS, TB, VEC, NV, true, true>
+           : sum0  ? norm_grad_kernel<TS, TB, VEC, NV, false, true>
+                   : norm_grad_kernel<TS, TB, VEC, NV, false, false>;
+  return launch_rows(k, plan[which], s, P, VEC ? (int64_t)s.threads * (NV ? NV : 1) * 8 * 2 * (sizeof(TS) + sizeof(TB)) : 0,
+                                 P.bias ? P.dim * 4 : 0, MAX_PARTS, stream);
+}
+
+struct Gradient {
+  const NormParams& P;
+  const Shape& s;
+  bool sum0;
+  cudaStream_t stream;
+  template <typename TS, typename TB, int VEC, int NV>
+  int operator()() const {
+    return run_grad<TS, TB, VEC, NV>(P, s, sum0, stream);
+  }
+};
+
+}  // namespace
+}  // namespace dp
+
+using namespace dp;
+
+extern "C" {
+
+size_t dp_block_norm_workspace_size(int64_t rows, int64_t dim) {
+  if (rows < 0 || rows > INT32_MAX || dim < 1 || dim > DP_MAX_NORM_DIM) {
+    op_fail(DP_ERR_INVALID_ARG, "rows = %lld or dim = %lld out of range", (long long)rows, (long long)dim);
+    return 0;
+  }
+  const int64_t parts = rows < MAX_PARTS ? rows + 1 : MAX_PARTS;
+  return (size_t)(parts * 4 * dim * 4 + 255) / 256 * 256;
+}
+
+dp_status_t dp_block_norm_grad(const dp_block_norm_t* p, void* dx, void* dy, const void* dr, const void* dz,
+                               const void* r, const void* y, const void* w_post, const void* b_post, const void* gate,
+                               const void* w_pre, const float* post_stats, const float* pre_stats, void* dw_post,
+                               void* db_post, void* dgate, void* dw_pre, void* db_pre, void* ws, dp_stream_t stream_) {
+  DP_TRY(check_norm(p, y != nullptr, gate != nullptr));
+  const bool some = p->rows > 0, pre = (p->norms & DP_NORM_PRE) != 0, post = (p->norms & DP_NORM_POST) != 0;
+  const int es = elem_size(p->stream_dtype), eb = elem_size(p->block_dtype), ep = elem_size(p->param_dtype);
+  DP_TRY(check_dev(dx, es, some, "dx"));
+  DP_TRY(check_dev(dy, eb, some && y, "dy"));
+  DP_TRY(check_dev(dr, es, false, "dr"));
+  DP_TRY(check_dev(dz, eb, some && pre, "dz"));
+  DP_TRY(check_dev(r, es, some && pre, "r"));
+  DP_TRY(check_dev(y, eb, false, "y"));
+  if (some && !y && dy) return op_fail(DP_ERR_INVALID_ARG, "dy must be NULL without y");
+  DP_TRY(check_dev(w_post, ep, false, "w_post"));
+  DP_TRY(check_dev(b_post, ep, false, "b_post"));
+  DP_TRY(check_dev(gate, ep, false, "gate"));
+  DP_TRY(check_dev(w_pre, ep, false, "w_pre"));
+  DP_TRY(check_dev(post_stats, 8, some && post, "post_stats"));
+  DP_TRY(check_dev(pre_stats, 8, some && pre, "pre_stats"));
+  DP_TRY(check_dev(dw_post, ep, false, "dw_post"));
+  DP_TRY(check_dev(db_post, ep, false, "db_post"));
+  DP_TRY(check_dev(dgate, ep, false, "dgate"));
+  DP_TRY(check_dev(dw_pre, ep, false, "dw_pre"));
+  DP_TRY(check_dev(db_pre, ep, false, "db_pre"));
+  if (!post && (dw_post || db_post)) return op_fail(DP_ERR_INVALID_ARG, "dw_post and db_post need DP_NORM_POST");
+  if (!pre && (dw_pre || db_pre)) return op_fail(DP_ERR_INVALID_ARG, "dw_pre and db_pre need DP_NORM_PRE");
+  if (p->gate_mode == DP_GATE_NONE && dgate) return op_fail(DP_ERR_INVALID_ARG, "dgate needs a gate");
+  DP_TRY(check_dev(ws, 256, some, "ws"));
+  const cudaStream_t stream = (cudaStream_t)stream_;
+  NvtxRange range("block norm gradient");
+  int64_t parts = 0;
+  int launches = 0;
+  // S0 and P0 are summed for the biases' gradients, and for a channel gate's where the post norm has a bias.
+  const bool sum0 = p->kind == DP_NORM_LAYER || db_post || db_pre || (dgate && post && b_post);
+  if (some) {
+    const Shape s = shape_of(p->dim);
+    NormParams P = base_params(*p, s);
+    P.dx = dx;
+    P.dy = dy;
+    P.dr = dr;
+    P.dz = dz;
+    P.x = r;
+    P.y = y;
+    P.w_post = post ? w_post : nullptr;
+    P.b_post = post ? b_post : nullptr;
+    P.gate = gate;
+    P.w_pre = w_pre;
+    P.post_stats = reinterpret_cast<float2*>(const_cast<float*>(post_stats));
+    P.pre_stats = reinterpret_cast<float2*>(const_cast<float*>(pre_stats));
+    P.dgate_token = p->gate_mode == DP_GATE_TOKEN ? dgate : nullptr;
+    P.part = static_cast<float*>(ws);
+    P.bias = P.dgate_token && P.b_post;
+    parts = dispatch(*p, p->dim % 8 == 0 && slots_fit(*p, s, 2) && all16({dx, dy, dr, dz, r, y}), s.group <= 32 ? 0 : s.nv, Gradient{P, s, sum0, stream});
+    ++launches;
+  }
+  FinishParams F = {};
+  F.part = static_cast<const float*>(ws);
+  F.parts = parts;
+  F.dim = p->dim;
+  F.sum0 = sum0;
+  F.gate_mode = p->gate_mode;
+  F.pdt = p->param_dtype;
+  F.accumulate = p->accumulate;
+  F.w_post = post ? w_post : nullptr;
+  F.b_post = post ? b_post : nullptr;
+  F.gate = gate;
+  F.dw_post = dw_post;
+  F.db_post = db_post;
+  F.dgate = p->gate_mode == DP_GATE_CHANNEL ? dgate : nullptr;
+  F.dw_pre = dw_pre;
+  F.db_pre = db_pre;
+  F.b = p->branch_scale;
+  if (F.dw_post || F.db_post || F.dgate || F.dw_pre || F.db_pre) {
+    const cudaError_t e = launch_after(norm_finish_kernel, (p->dim + FIN_COLS - 1) / FIN_COLS, dim3(FIN_COLS, FIN_ROWS), stream, F);
+    if (e != cudaSuccess) return op_fail(DP_ERR_CUDA, "block norm gradient launch: %s", cudaGetErrorString(e));
+    ++launches;
+  }
+  return launches ? op_launched("block norm gradient launch", launches) : DP_OK;
+}
+
+}  // extern "C"
