@@ -102,12 +102,13 @@ __device__ __forceinline__ void places_of(const Walk& W, Place (&p)[U]) {
   }
 }
 
-// Pieces that are not there, or lie beyond the row's end, are zeros.  vec: dim is a multiple of 8 and rows 16-byte aligned.
+// Pieces that are not there, or lie beyond the row's end, are zeros.  VEC: dim is a multiple of 8 and rows 16-byte aligned (the
+// general way needs registers that cost the kernels a third of their threads).
 __device__ __forceinline__ int there(const Place& p, int dim) { return p.on ? there8(p.col, dim) : 0; }
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_piece(const T* base, int64_t ld, const Place& p, const Walk& W, int vec) {
+template <int VEC, typename T>
+__device__ __forceinline__ Raw8<T> load_piece(const T* base, int64_t ld, const Place& p, const Walk& W) {
   const T* q = base + p.row * ld + p.col;
-  if (vec) {
+  if (VEC) {
     if (p.on && p.col < W.dim) return load_raw8(q);
     const float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     Raw8<T> w;
@@ -116,12 +117,12 @@ __device__ __forceinline__ Raw8<T> load_piece(const T* base, int64_t ld, const P
   }
   return load_any8(q, there(p, W.dim), base, base + (W.rows - 1) * ld + W.dim);
 }
-template <typename T>
-__device__ __forceinline__ void store_piece(T* base, int64_t ld, const Place& p, const Walk& W, int vec, const f2_t (&v)[4]) {
+template <int VEC, typename T>
+__device__ __forceinline__ void store_piece(T* base, int64_t ld, const Place& p, const Walk& W, const f2_t (&v)[4]) {
   T* q = base + p.row * ld + p.col;
   Raw8<T> o;
   o.pack2(v);
-  if (!vec) store_any8(q, there(p, W.dim), o);
+  if (!VEC) store_any8(q, there(p, W.dim), o);
   else if (p.on && p.col < W.dim) store_raw8(q, o);
 }
 struct Ckpt {
@@ -150,13 +151,13 @@ __device__ __forceinline__ Kept get_ckpt(const Ckpt& c, const Place& p, int pitc
 
 constexpr int COPY_U = 4, ACT_U = 3;  // pieces of a thread (8k x 11008: 1 137 + 146, 2 121 + 152, 3 121 + 149, 4 125 + 160 us)
 
-template <typename T>
-__global__ void __launch_bounds__(THREADS) encode_kernel(Ckpt c, const T* x, int64_t ldx, Walk W, int vec) {
+template <typename T, int VEC>
+__global__ void __launch_bounds__(THREADS) encode_kernel(Ckpt c, const T* x, int64_t ldx, Walk W) {
   Place p[COPY_U];
   Raw8<T> w[COPY_U];
   places_of(W, p);
 #pragma unroll
-  for (int i = 0; i < COPY_U; ++i) w[i] = load_piece(x, ldx, p[i], W, vec);
+  for (int i = 0; i < COPY_U; ++i) w[i] = load_piece<VEC>(x, ldx, p[i], W);
 #pragma unroll
   for (int i = 0; i < COPY_U; ++i) {
     f2_t v[4];
@@ -164,8 +165,8 @@ __global__ void __launch_bounds__(THREADS) encode_kernel(Ckpt c, const T* x, int
     put_ckpt(c, p[i], W.pieces * 8, w[i], v);
   }
 }
-template <typename T>
-__global__ void __launch_bounds__(THREADS) decode_kernel(T* x, int64_t ldx, Ckpt c, Walk W, int vec) {
+template <typename T, int VEC>
+__global__ void __launch_bounds__(THREADS) decode_kernel(T* x, int64_t ldx, Ckpt c, Walk W) {
   grid_go();  // a product of the decoded rows may be set up meanwhile
   Place p[COPY_U];
   Kept k[COPY_U];
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(T* x, int64_t ldx, Ckpt
   for (int i = 0; i < COPY_U; ++i) {
     f2_t v[4];
     values_of(k[i].codes, k[i].E, v);
-    store_piece(x, ldx, p[i], W, vec, v);
+    store_piece<VEC>(x, ldx, p[i], W, v);
   }
 }
 
@@ -228,16 +229,16 @@ __device__ __forceinline__ void act_of(f2_t g, f2_t& f, f2_t& df) {
   }
 }
 
-template <int ACT, bool GATED>
+template <int ACT, bool GATED, int VEC>
 __global__ void __launch_bounds__(THREADS) act_kernel(bf16_t* h, const bf16_t* g, const bf16_t* u, Ckpt g8, Ckpt u8,
-                                                      int64_t ld, int64_t ldh, Walk W, int vec) {
+                                                      int64_t ld, int64_t ldh, Walk W) {
   Place p[ACT_U];
   Raw8<bf16_t> gw[ACT_U], uw[ACT_U];
   places_of(W, p);
 #pragma unroll
   for (int i = 0; i < ACT_U; ++i) {
-    gw[i] = load_piece(g, ld, p[i], W, vec);
-    if (GATED) uw[i] = load_piece(u, ld, p[i], W, vec);
+    gw[i] = load_piece<VEC>(g, ld, p[i], W);
+    if (GATED) uw[i] = load_piece<VEC>(u, ld, p[i], W);
   }
 #pragma unroll
   for (int i = 0; i < ACT_U; ++i) {
@@ -254,20 +255,20 @@ __global__ void __launch_bounds__(THREADS) act_kernel(bf16_t* h, const bf16_t* g
       act_of<ACT>(gv[k], f, unused);
       gv[k] = GATED ? f2_mul(f, uv[k]) : f;
     }
-    store_piece(h, ldh, p[i], W, vec, gv);
+    store_piece<VEC>(h, ldh, p[i], W, gv);
   }
 }
 
-template <int ACT, bool GATED>
+template <int ACT, bool GATED, int VEC>
 __global__ void __launch_bounds__(THREADS) act_grad_kernel(bf16_t* dg, bf16_t* du, bf16_t* h, const bf16_t* dh, Ckpt g8,
-                                                           Ckpt u8, int64_t ld, int64_t ldh, Walk W, int vec) {
+                                                           Ckpt u8, int64_t ld, int64_t ldh, Walk W) {
   Place p[ACT_U];
   Raw8<bf16_t> dw[ACT_U];
   Kept gk[ACT_U], uk[ACT_U];
   places_of(W, p);
 #pragma unroll
   for (int i = 0; i < ACT_U; ++i) {
-    dw[i] = load_piece(dh, ldh, p[i], W, vec);
+    dw[i] = load_piece<VEC>(dh, ldh, p[i], W);
     gk[i] = get_ckpt(g8, p[i], W.pieces * 8);
     if (GATED) uk[i] = get_ckpt(u8, p[i], W.pieces * 8);
   }
@@ -285,9 +286,9 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(bf16_t* dg, bf16_t* d
       gv[k] = f2_mul(GATED ? f2_mul(dv[k], uv[k]) : dv[k], df);
       dv[k] = f2_mul(dv[k], f);
     }
-    store_piece(dg, ld, p[i], W, vec, gv);
-    if (GATED) store_piece(du, ld, p[i], W, vec, dv);
-    if (h) store_piece(h, ldh, p[i], W, vec, hv);
+    store_piece<VEC>(dg, ld, p[i], W, gv);
+    if (GATED) store_piece<VEC>(du, ld, p[i], W, dv);
+    if (h) store_piece<VEC>(h, ldh, p[i], W, hv);
   }
 }
 
@@ -334,10 +335,11 @@ dp_status_t dp_ckpt8_encode(int8_t* codes, uint8_t* scales, const void* x, int64
   const Walk W = walk_of(rows, dim);
   const int vec = dim % 8 == 0 && rows16(x, ldx, e);
   NvtxRange range("checkpoint encode");
+  const Ckpt c{codes, scales};
   if (dtype == DP_BF16)
-    encode_kernel<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>(Ckpt{codes, scales}, (const bf16_t*)x, ldx, W, vec);
+    (vec ? encode_kernel<bf16_t, 1> : encode_kernel<bf16_t, 0>)<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>(c, (const bf16_t*)x, ldx, W);
   else
-    encode_kernel<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>(Ckpt{codes, scales}, (const float*)x, ldx, W, vec);
+    (vec ? encode_kernel<float, 1> : encode_kernel<float, 0>)<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>(c, (const float*)x, ldx, W);
   return op_launched("checkpoint encode launch", 1);
 }
 
@@ -355,9 +357,9 @@ dp_status_t dp_ckpt8_decode(void* x, const int8_t* codes, const uint8_t* scales,
   const int vec = dim % 8 == 0 && rows16(x, ldx, e);
   NvtxRange range("checkpoint decode");
   if (dtype == DP_BF16)
-    decode_kernel<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>((bf16_t*)x, ldx, c, W, vec);
+    (vec ? decode_kernel<bf16_t, 1> : decode_kernel<bf16_t, 0>)<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>((bf16_t*)x, ldx, c, W);
   else
-    decode_kernel<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>((float*)x, ldx, c, W, vec);
+    (vec ? decode_kernel<float, 1> : decode_kernel<float, 0>)<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>((float*)x, ldx, c, W);
   return op_launched("checkpoint decode launch", 1);
 }
 
@@ -378,10 +380,13 @@ dp_status_t dp_act_ckpt8(uint16_t* h, const uint16_t* g, const uint16_t* u, int8
   const Walk W = walk_of(rows, dim);
   const int vec = dim % 8 == 0 && rows16(g, ld, 2) && rows16(u, ld, 2) && rows16(h, ldh, 2);
   const Ckpt a{g8, g8_scales}, b{u8, u8_scales};
-  auto k = act == DP_ACT_SILU ? (u ? act_kernel<DP_ACT_SILU, true> : act_kernel<DP_ACT_SILU, false>)
-                              : (u ? act_kernel<DP_ACT_GELU, true> : act_kernel<DP_ACT_GELU, false>);
+  auto pick = [&](auto one, auto zero) { return vec ? one : zero; };
+  auto k = act == DP_ACT_SILU ? (u ? pick(act_kernel<DP_ACT_SILU, true, 1>, act_kernel<DP_ACT_SILU, true, 0>)
+                                   : pick(act_kernel<DP_ACT_SILU, false, 1>, act_kernel<DP_ACT_SILU, false, 0>))
+                              : (u ? pick(act_kernel<DP_ACT_GELU, true, 1>, act_kernel<DP_ACT_GELU, true, 0>)
+                                   : pick(act_kernel<DP_ACT_GELU, false, 1>, act_kernel<DP_ACT_GELU, false, 0>));
   NvtxRange range("activation with checkpoint");
-  k<<<grid_of(W, ACT_U), THREADS, 0, (cudaStream_t)stream>>>(h, g, u, a, b, ld, ldh, W, vec);
+  k<<<grid_of(W, ACT_U), THREADS, 0, (cudaStream_t)stream>>>(h, g, u, a, b, ld, ldh, W);
   return op_launched("activation launch", 1);
 }
 
@@ -404,10 +409,13 @@ dp_status_t dp_act_ckpt8_grad(uint16_t* dg, uint16_t* du, uint16_t* h, const uin
   const int vec = dim % 8 == 0 && rows16(dg, ld, 2) && rows16(du, ld, 2) && rows16(h, ldh, 2) && rows16(dh, ldh, 2);
   const Ckpt a{const_cast<int8_t*>(g8), const_cast<uint8_t*>(g8_scales)};
   const Ckpt b{const_cast<int8_t*>(u8), const_cast<uint8_t*>(u8_scales)};
-  auto k = act == DP_ACT_SILU ? (u8 ? act_grad_kernel<DP_ACT_SILU, true> : act_grad_kernel<DP_ACT_SILU, false>)
-                              : (u8 ? act_grad_kernel<DP_ACT_GELU, true> : act_grad_kernel<DP_ACT_GELU, false>);
+  auto pick = [&](auto one, auto zero) { return vec ? one : zero; };
+  auto k = act == DP_ACT_SILU ? (u8 ? pick(act_grad_kernel<DP_ACT_SILU, true, 1>, act_grad_kernel<DP_ACT_SILU, true, 0>)
+                                    : pick(act_grad_kernel<DP_ACT_SILU, false, 1>, act_grad_kernel<DP_ACT_SILU, false, 0>))
+                              : (u8 ? pick(act_grad_kernel<DP_ACT_GELU, true, 1>, act_grad_kernel<DP_ACT_GELU, true, 0>)
+                                    : pick(act_grad_kernel<DP_ACT_GELU, false, 1>, act_grad_kernel<DP_ACT_GELU, false, 0>));
   NvtxRange range("activation gradient");
-  k<<<grid_of(W, ACT_U), THREADS, 0, (cudaStream_t)stream>>>(dg, du, h, dh, a, b, ld, ldh, W, vec);
+  k<<<grid_of(W, ACT_U), THREADS, 0, (cudaStream_t)stream>>>(dg, du, h, dh, a, b, ld, ldh, W);
   return op_launched("activation gradient launch", 1);
 }
 

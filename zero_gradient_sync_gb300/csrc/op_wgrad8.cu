@@ -161,16 +161,25 @@ __device__ __forceinline__ Item item_at(const WgradParams& P, int32_t item) {
 // Up to 32 rows of one column of a warp's block to memory.  Adding in fp32 is left to the L2: each element gets one
 // addition a call, so nothing depends on an order, and nobody waits for the old value.  bf16 has to be added in fp32 and
 // rounded once, so its old values are read, all 32 rows in flight (the sums of the block are in shared memory by then).
+template <bool ADD16>
 __device__ __forceinline__ void store_block(const WgradParams& P, int32_t part, int32_t row0, int32_t col0, int32_t r0,
                                             int32_t c, const float* block, int rows) {
   if (part < 0 && P.dtype == DP_BF16) {
     bf16_t* dst = static_cast<bf16_t*>(P.dw) + (int64_t)(row0 + r0) * P.k + col0 + c;
-    uint16_t old[32];
+    if (ADD16) {
+      uint16_t old[32];
 #pragma unroll
-    for (int r = 0; r < 32; ++r) old[r] = P.accumulate && r < rows ? dst[r * P.k] : (uint16_t)0;
+      for (int r = 0; r < 32; ++r) old[r] = r < rows ? dst[r * P.k] : (uint16_t)0;
 #pragma unroll
-    for (int r = 0; r < 32; ++r)
-      if (r < rows) dst[r * P.k] = bf16_rn(__fadd_rn(bf16_to_f32(old[r]), block[r * 33]));
+      for (int r = 0; r < 32; ++r)
+        if (r < rows) dst[r * P.k] = bf16_rn(__fadd_rn(bf16_to_f32(old[r]), block[r * 33]));
+    } else {
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) {
+        *dst = bf16_rn(block[r * 33]);
+        dst += P.k;
+      }
+    }
     return;
   }
   const int64_t ld = part >= 0 ? BN : P.k;
@@ -186,6 +195,8 @@ __device__ __forceinline__ void store_block(const WgradParams& P, int32_t part, 
   }
 }
 
+// ADD16: the result is added to bf16 (a variant of its own: its 32 old values cost the others registers).
+template <bool ADD16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     wgrad8_kernel(const __grid_constant__ WgradParams P, const __grid_constant__ CUtensorMap map_dy,
                   const __grid_constant__ CUtensorMap map_x) {
@@ -331,7 +342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __syncwarp();
         // Row by row: 32 lanes, 32 consecutive columns.
         const int col = half * 128 + c + lane;
-        if (it.col0 + col < P.k) store_block(P, it.part, it.row0, it.col0, r0, col, mine + lane, rows);
+        if (it.col0 + col < P.k) store_block<ADD16>(P, it.part, it.row0, it.col0, r0, col, mine + lane, rows);
       }
     }
   }
@@ -501,11 +512,12 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
   CUtensorMap map_x, map_dy;
   DP_TRY(map_of(&map_x, base, pitch, rows, pitch));
   DP_TRY(map_of(&map_dy, aligned ? (const void*)dy : base + w.dy, n, rows, aligned ? lddy : w.lddy));
-  static thread_local int ready = -1;  // the device whose kernel has its shared memory granted
+  static thread_local int ready = -1;  // the device whose kernels have their shared memory granted
   int device = 0;
   cudaGetDevice(&device);
   if (ready != device) {
-    const cudaError_t attr = cudaFuncSetAttribute(wgrad8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t attr = cudaFuncSetAttribute(wgrad8_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (attr == cudaSuccess) attr = cudaFuncSetAttribute(wgrad8_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (attr != cudaSuccess) return op_fail(DP_ERR_CUDA, "weight gradient: %s", cudaGetErrorString(attr));
     ready = device;
   }
@@ -543,7 +555,8 @@ dp_status_t dp_wgrad8(void* dw, const uint16_t* dy, const int8_t* codes, const u
   a[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = a;
   c.numAttrs = 1;
-  cudaError_t err = cudaLaunchKernelEx(&c, wgrad8_kernel, P, map_dy, map_x);
+  cudaError_t err = accumulate && dtype == DP_BF16 ? cudaLaunchKernelEx(&c, wgrad8_kernel<true>, P, map_dy, map_x)
+                                                  : cudaLaunchKernelEx(&c, wgrad8_kernel<false>, P, map_dy, map_x);
   if (err == cudaSuccess && s.slices > 1) {
     err = launch_after(wgrad8_join_kernel, s.left * (BM / 4), dim3(BN), stream, P);
     ++launches;
