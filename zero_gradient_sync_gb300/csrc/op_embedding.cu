@@ -42,7 +42,7 @@ __host__ __device__ inline int64_t up64(int64_t x) { return (x + 63) & ~int64_t(
 inline int chunk_of(int64_t tokens, int64_t dim) {
   const int64_t slabs = (dim + COLS - 1) / COLS;
   for (int c = 32; c > 8; c >>= 1)
-    if ((tokens + c - 1) / c * slabs >= 148 * 16) return c;
+    if ((tokens + c - 1) / c * slabs >= 148 * 8) return c;
   return 8;
 }
 inline EmbWs emb_ws(int64_t tokens, int64_t dim) {
