@@ -125,6 +125,14 @@ __device__ __forceinline__ void load_param(const void* p, int dtype, float none,
 // `buf` (zero beyond the group's warps), so one barrier a call is enough: a half is written again only after the barrier
 // of the call in between.  The warps' sums are read as broadcast words, which takes less than another five shuffles.
 typedef float GroupBuf[2][3][16];
+__device__ __forceinline__ float sum4(float4 a) { return (a.x + a.y) + (a.z + a.w); }
+__device__ __forceinline__ float warps_sum(const float* of, int group) {
+  const float4* p = reinterpret_cast<const float4*>(of);
+  float s = sum4(p[0]);
+  if (group > 128) s += sum4(p[1]);
+  if (group > 256) s += sum4(p[2]) + sum4(p[3]);
+  return s;
+}
 template <int N, bool SMALL>
 __device__ __forceinline__ void group_sum(float (&v)[N], int group, GroupBuf& buf, int& half) {
 #pragma unroll
@@ -141,11 +149,7 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int group, GroupBuf& bu
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float4* p = reinterpret_cast<const float4*>(buf[half][i]);
-    const float4 a = p[0], b = p[1], c = p[2], d = p[3];
-    v[i] = (((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w))) + (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
-  }
+  for (int i = 0; i < N; ++i) v[i] = warps_sum(buf[half][i], group);
   half ^= 1;
 }
 __device__ __forceinline__ void clear(GroupBuf& buf) {
@@ -153,42 +157,58 @@ __device__ __forceinline__ void clear(GroupBuf& buf) {
   __syncthreads();
 }
 
-// Mean (0 for RMS) and 1 / sqrt(var + eps) of a row held in registers, which is centred on the way.  Pieces beyond dim hold
-// zeros, before and after.
-template <int VEC, int NV, bool LAYER, bool SMALL>
-__device__ __forceinline__ float2 row_stats(f2_t (&v)[NV][4], float eps, float inv, int tid, int group, int dim, GroupBuf& buf,
-                                            int& half) {
-  float s[1], mean = 0.0f;
-  f2_t sum = f2_both(0.0f);
-  if (LAYER) {
+// v + by, for the elements that the row has.
+template <int VEC, int NV>
+__device__ __forceinline__ void shift_row(f2_t (&v)[NV][4], float by, int tid, int group, int dim) {
+  const f2_t b2 = f2_both(by);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    const int c = col_of(tid, group, j, 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum = f2_add(sum, v[j][k]);
-    s[0] = f2_sum(sum);
-    group_sum<1, SMALL>(s, group, buf, half);
-    mean = s[0] * inv;
-    const f2_t less = f2_both(-mean);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (VEC) {
-          if (col_of(tid, group, j, 0) < dim) v[j][k] = f2_add(v[j][k], less);
-        } else {
-          float a, b;
-          f2_unpack(v[j][k], a, b);
-          v[j][k] = f2_pack(col_of(tid, group, j, 2 * k) < dim ? a - mean : 0.0f,
-                            col_of(tid, group, j, 2 * k + 1) < dim ? b - mean : 0.0f);
-        }
+    for (int k = 0; k < 4; ++k) {
+      if (VEC) {
+        if (c < dim) v[j][k] = f2_add(v[j][k], b2);
+      } else {
+        float a, b;
+        f2_unpack(v[j][k], a, b);
+        v[j][k] = f2_pack(c + 2 * k < dim ? a + by : 0.0f, c + 2 * k + 1 < dim ? b + by : 0.0f);
       }
-    sum = f2_both(0.0f);
+    }
   }
+}
+template <int NV>
+__device__ __forceinline__ float row_sum(const f2_t (&v)[NV][4]) {
+  f2_t sum = f2_both(0.0f);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum = f2_add(sum, v[j][k]);
+  return f2_sum(sum);
+}
+template <int NV>
+__device__ __forceinline__ float row_squares(const f2_t (&v)[NV][4]) {
+  f2_t sum = f2_both(0.0f);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum = f2_fma(v[j][k], v[j][k], sum);
-  s[0] = f2_sum(sum);
+  return f2_sum(sum);
+}
+
+// Mean (0 for RMS) and 1 / sqrt(var + eps) of a row held in registers, which is centred on the way.  Pieces beyond dim hold
+// zeros, before and after.  (A layer norm with one barrier, from each warp's own mean and the squares about it, takes more
+// instructions than the barrier is worth: 32768 x 1024 forward 95 us against 75.)
+template <int VEC, int NV, bool LAYER, bool SMALL>
+__device__ __forceinline__ float2 row_stats(f2_t (&v)[NV][4], float eps, float inv, int tid, int group, int dim, GroupBuf& buf,
+                                            int& half) {
+  float mean = 0.0f, s[1];
+  if (LAYER) {
+    s[0] = row_sum<NV>(v);
+    group_sum<1, SMALL>(s, group, buf, half);
+    mean = s[0] * inv;
+    shift_row<VEC, NV>(v, -mean, tid, group, dim);
+  }
+  s[0] = row_squares<NV>(v);
   group_sum<1, SMALL>(s, group, buf, half);
   return make_float2(mean, 1.0f / sqrtf(fmaf(s[0], inv, eps)));
 }
