@@ -331,7 +331,7 @@ NormParams base_params(const dp_block_norm_t& p, const Shape& s) {
 
 // Whether one row of a CTA fits its shared memory (`pairs` rows of the stream and of the block).
 bool slots_fit(const dp_block_norm_t& p, const Shape& s, int pairs) {
-  return (int64_t)s.threads * s.nv * 8 * pairs * (elem_size(p.stream_dtype) + elem_size(p.block_dtype)) + 4 * p.dim <= 220 * 1024;
+  return (int64_t)s.threads * s.nv * 8 * pairs * (elem_size(p.stream_dtype) + elem_size(p.block_dtype)) + 4 * p.dim + s.threads * 2 <= 220 * 1024;
 }
 
 bool all16(std::initializer_list<const void*> ps) {

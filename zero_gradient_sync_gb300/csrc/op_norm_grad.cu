@@ -30,7 +30,9 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
   const int64_t row0 = (int64_t)blockIdx.x * per_cta + which, step = (int64_t)gridDim.x * per_cta;
   const int group = P.group, dim = P.dim;
   const int at_dz = RowB::bytes(group), at_r = 2 * at_dz, at_dr = at_r + RowS::bytes(group);
-  const int slot_bytes = at_dr + RowS::bytes(group);
+  // Each warp's copy of the row's statistics.  (As register loads a row ahead they cost 32768 x 1024 a third more time: waits
+  // for shared memory then wait for them too.)
+  const int at_st = at_dr + RowS::bytes(group), part = SMALL ? group : 32, slot_bytes = at_st + group / part * 16;
   char* mine = slots + which * P.slots * slot_bytes;
   auto fetch = [&](int64_t row, int slot) {
     if (VEC) __syncwarp();  // the slot's last row has been read
@@ -42,6 +44,11 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
         RowS::fetch(to + at_r, static_cast<const TS*>(P.x) + row * dim, tid, group, dim);
       }
       if (P.dr) RowS::fetch(to + at_dr, static_cast<const TS*>(P.dr) + row * dim, tid, group, dim);
+      if ((tid & (part - 1)) == 0) {
+        to += at_st + tid / part * 16;
+        if (P.pre) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(P.pre_stats + row) : "memory");
+        if (P.post) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to + 8)), "l"(P.post_stats + row) : "memory");
+      }
     }
     if (VEC) fetched();
   };
@@ -84,13 +91,9 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
     }
   }
   const float inv = 1.0f / (float)dim;
-  // The next row's statistics are loaded a row ahead, like its elements.
-  float2 next_pre = make_float2(0.0f, 1.0f), next_post = make_float2(0.0f, 1.0f);
   uint32_t next_gate = P.pdt == DP_BF16 ? 0x3f80u : 0x3f800000u;  // as it lies in memory: a conversion would wait for it
   auto scalars = [&](int64_t row) {
     if (row >= P.rows) return;
-    if (P.pre) next_pre = P.pre_stats[row];
-    if (P.post) next_post = P.post_stats[row];
     if (token) next_gate = P.pdt == DP_BF16 ? __ldg(static_cast<const uint16_t*>(P.gate) + row) : __ldg(static_cast<const uint32_t*>(P.gate) + row);
   };
   scalars(row0);
@@ -100,12 +103,14 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_grad_kernel(const __grid_co
     const bool live = !SMALL || row < P.rows;
     const int row_dim = live ? dim : 0;
     fetch(row + (P.slots - 1) * step, slot == 0 ? P.slots - 1 : slot - 1);
-    const float2 pre = next_pre, post = next_post;
     const float gt = __uint_as_float(P.pdt == DP_BF16 ? next_gate << 16 : next_gate);
     scalars(row + step);
     if (VEC) fetch_wait(P.slots - 1);
     const char* here = mine + slot * slot_bytes;
     if (++slot == P.slots) slot = 0;
+    float2 pre = make_float2(0.0f, 1.0f), post = pre;
+    if (live && P.pre) pre = VEC ? *reinterpret_cast<const float2*>(here + at_st + tid / part * 16) : P.pre_stats[row];
+    if (live && P.post) post = VEC ? *reinterpret_cast<const float2*>(here + at_st + tid / part * 16 + 8) : P.post_stats[row];
     f2_t D[NV][4];
     RowB yr;
     if (has_y && !VEC) yr.load(here, static_cast<const TB*>(P.y), row * dim, static_cast<const TB*>(P.y) + P.rows * dim, tid, group, row_dim);
@@ -312,7 +317,7 @@ int run_grad(NormParams P, const Shape& s, bool sum0, cudaStream_t stream) {
   auto k = P.layer ? norm_grad_kernel<TS, TB, VEC, NV, true, true>
            : sum0  ? norm_grad_kernel<TS, TB, VEC, NV, false, true>
                    : norm_grad_kernel<TS, TB, VEC, NV, false, false>;
-  return launch_rows(k, plan[which], s, P, VEC ? (int64_t)s.threads * (NV ? NV : 1) * 8 * 2 * (sizeof(TS) + sizeof(TB)) : 0,
+  return launch_rows(k, plan[which], s, P, VEC ? (int64_t)s.threads * (NV ? NV : 1) * 8 * 2 * (sizeof(TS) + sizeof(TB)) + s.threads / 2 * (s.group < 32 ? 32 / s.group : 1) : 0,
                                  P.bias ? P.dim * 4 : 0, MAX_PARTS, stream);
 }
 
