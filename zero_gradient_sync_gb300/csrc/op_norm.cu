@@ -4,7 +4,9 @@
 //
 // Apart, these are two norms, a product and a scaled sum: x, y, r and the post norm's output go through memory several
 // times.  Here a row stays in registers from y to z: x and y are read once, r and z written once (four row passes
-// forward; six backward: dr, dz, r, y in, dx, dy out).  What bounds both is memory.
+// forward; six backward: dr, dz, r, y in, dx, dy out).  What bounds both is memory, and next to it the two to four sums over
+// a row that have to be waited for.  Measured, as a share of the copy rate: rms forward 0.69 to 0.72 in bf16 (32768 x 1024: 56
+// us), 0.88 with an fp32 stream; layer norms 0.48 to 0.59 and 0.62 to 0.79.
 //
 // A row is held by a group of threads, eight consecutive elements each, NV such pieces a thread.  A group is 8, 16 or 32 lanes
 // up to 256 columns (SMALL: a CTA has several), else the whole CTA.  CTAs are persistent, so parameters are

