@@ -152,32 +152,34 @@ __device__ __forceinline__ Kept get_ckpt(const Ckpt& c, const Place& p, int pitc
   return k;
 }
 
-constexpr int COPY_U = 4, ACT_U = 3;  // pieces of a thread (8k x 11008: 1 137 + 146, 2 121 + 152, 3 121 + 149, 4 125 + 160 us)
+// Pieces of a thread.  Activations 8k x 11008: 1 137 + 146, 2 121 + 152, 3 121 + 149, 4 125 + 160 us.  Encoding and decoding: 4,
+// and 1 where four would leave SMs without work (129 x 1111 encoded: 7.3 us with 4, 3.2 with 1).
+constexpr int COPY_U = 4, ACT_U = 3;
 
-template <typename T, int VEC>
+template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(THREADS) encode_kernel(Ckpt c, const T* x, int64_t ldx, Walk W) {
-  Place p[COPY_U];
-  Raw8<T> w[COPY_U];
+  Place p[U];
+  Raw8<T> w[U];
   places_of(W, p);
 #pragma unroll
-  for (int i = 0; i < COPY_U; ++i) w[i] = load_piece<VEC>(x, ldx, p[i], W);
+  for (int i = 0; i < U; ++i) w[i] = load_piece<VEC>(x, ldx, p[i], W);
 #pragma unroll
-  for (int i = 0; i < COPY_U; ++i) {
+  for (int i = 0; i < U; ++i) {
     f2_t v[4];
     w[i].unpack2(v);
     put_ckpt(c, p[i], W.pieces * 8, w[i], v);
   }
 }
-template <typename T, int VEC>
+template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(THREADS) decode_kernel(T* x, int64_t ldx, Ckpt c, Walk W) {
   grid_go();  // a product of the decoded rows may be set up meanwhile
-  Place p[COPY_U];
-  Kept k[COPY_U];
+  Place p[U];
+  Kept k[U];
   places_of(W, p);
 #pragma unroll
-  for (int i = 0; i < COPY_U; ++i) k[i] = get_ckpt(c, p[i], W.pieces * 8);
+  for (int i = 0; i < U; ++i) k[i] = get_ckpt(c, p[i], W.pieces * 8);
 #pragma unroll
-  for (int i = 0; i < COPY_U; ++i) {
+  for (int i = 0; i < U; ++i) {
     f2_t v[4];
     values_of(k[i].codes, k[i].E, v);
     store_piece<VEC>(x, ldx, p[i], W, v);
@@ -315,6 +317,21 @@ dp_status_t check_ckpt(const int8_t* codes, const uint8_t* scales, bool needed, 
 }
 Walk walk_of(int64_t rows, int64_t dim) { return Walk{rows, (int)(dp_ckpt8_pitch(dim) / 8), (int)dim}; }
 unsigned grid_of(const Walk& W, int u) { return (unsigned)((W.rows * W.pieces + THREADS * u - 1) / (THREADS * u)); }
+struct Encode {
+  template <typename T, int VEC, int U>
+  static constexpr auto kernel = encode_kernel<T, VEC, U>;
+};
+struct Decode {
+  template <typename T, int VEC, int U>
+  static constexpr auto kernel = decode_kernel<T, VEC, U>;
+};
+template <typename T, typename K, typename... A>
+void copy_with(const Walk& W, bool vec, cudaStream_t stream, A... args) {
+  const bool few = W.rows * W.pieces <= (int64_t)sm_count() * THREADS * COPY_U;
+  auto k = vec ? (few ? K::template kernel<T, 1, 1> : K::template kernel<T, 1, COPY_U>)
+               : (few ? K::template kernel<T, 0, 1> : K::template kernel<T, 0, COPY_U>);
+  k<<<grid_of(W, few ? 1 : COPY_U), THREADS, 0, stream>>>(args...);
+}
 bool rows16(const void* p, int64_t ld, int size) { return is_aligned(p, 16) && ld * size % 16 == 0; }
 
 }  // namespace
@@ -339,10 +356,8 @@ dp_status_t dp_ckpt8_encode(int8_t* codes, uint8_t* scales, const void* x, int64
   const int vec = dim % 8 == 0 && rows16(x, ldx, e);
   NvtxRange range("checkpoint encode");
   const Ckpt c{codes, scales};
-  if (dtype == DP_BF16)
-    (vec ? encode_kernel<bf16_t, 1> : encode_kernel<bf16_t, 0>)<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>(c, (const bf16_t*)x, ldx, W);
-  else
-    (vec ? encode_kernel<float, 1> : encode_kernel<float, 0>)<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>(c, (const float*)x, ldx, W);
+  if (dtype == DP_BF16) copy_with<bf16_t, Encode>(W, vec, (cudaStream_t)stream, c, (const bf16_t*)x, ldx, W);
+  else copy_with<float, Encode>(W, vec, (cudaStream_t)stream, c, (const float*)x, ldx, W);
   return op_launched("checkpoint encode launch", 1);
 }
 
@@ -359,10 +374,8 @@ dp_status_t dp_ckpt8_decode(void* x, const int8_t* codes, const uint8_t* scales,
   const Ckpt c{const_cast<int8_t*>(codes), const_cast<uint8_t*>(scales)};
   const int vec = dim % 8 == 0 && rows16(x, ldx, e);
   NvtxRange range("checkpoint decode");
-  if (dtype == DP_BF16)
-    (vec ? decode_kernel<bf16_t, 1> : decode_kernel<bf16_t, 0>)<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>((bf16_t*)x, ldx, c, W);
-  else
-    (vec ? decode_kernel<float, 1> : decode_kernel<float, 0>)<<<grid_of(W, COPY_U), THREADS, 0, (cudaStream_t)stream>>>((float*)x, ldx, c, W);
+  if (dtype == DP_BF16) copy_with<bf16_t, Decode>(W, vec, (cudaStream_t)stream, (bf16_t*)x, ldx, c, W);
+  else copy_with<float, Decode>(W, vec, (cudaStream_t)stream, (float*)x, ldx, c, W);
   return op_launched("checkpoint decode launch", 1);
 }
 
