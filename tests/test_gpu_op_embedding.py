@@ -46,7 +46,8 @@ def test_lookup(dev, dtype, tokens, vocab, dim, off):
     (1, 1, 1, 0, torch.bfloat16, torch.int64), (1, 300, 768, 0, torch.bfloat16, torch.int32),
     (31, 3, 8, 0, torch.float32, torch.int64), (257, 70000, 16, 0, torch.bfloat16, torch.int64),
     (1000, 40, 77, 1, torch.bfloat16, torch.int32), (5000, 50257, 264, 0, torch.bfloat16, torch.int64),
-    (5000, 130, 768, 8, torch.float32, torch.int32), (20011, 1000, 256, 0, torch.bfloat16, torch.int64)])
+    (5000, 130, 768, 8, torch.float32, torch.int32), (20011, 1000, 256, 0, torch.bfloat16, torch.int64),
+    (200003, 70000, 8, 0, torch.float32, torch.int32), (140001, 40, 33, 1, torch.bfloat16, torch.int64)])
 def test_gradient(dev, kind, tokens, vocab, dim, off, dtype, id_type):
     gen = torch.Generator().manual_seed(tokens + vocab)
     ids = make_ids(kind, tokens, vocab, id_type, gen)

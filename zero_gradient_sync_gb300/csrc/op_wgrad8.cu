@@ -298,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!ok) {  // MMAs in flight end before the CTA may end
         volatile int none = 0;
         commit_pair(drained);
-        wait_bar(drained, 0, P.timeout_ns, &none);
+        wait_bar(drained, 0, 1000000000ull, &none);  // a second of its own, however short the limit that ran out
       }
     }
   } else if (warp >= EPI0) {
