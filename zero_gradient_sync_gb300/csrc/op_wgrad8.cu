@@ -266,6 +266,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (++s == STAGES) s = 0, phase ^= 1;
         }
       }
+      // The last steps' commits arrive here before the CTA may end: the other CTA's are remote.
+      for (int k = 0; ok && k < STAGES; ++k) {
+        ok = wait_bar(empty(s), phase ^ 1, P.timeout_ns, stop);
+        if (++s == STAGES) s = 0, phase ^= 1;
+      }
       if (!ok) {  // the copies in flight land before the CTA may end: a millisecond is far more than they take
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000) __nanosleep(1000);
